@@ -39,7 +39,7 @@
 extern "C" {
 #endif
 
-#define LIDX_ABI_VERSION 6
+#define LIDX_ABI_VERSION 7
 
 #if defined(__GNUC__)
 #define LIDX_API __attribute__((visibility("default")))
@@ -77,6 +77,8 @@ typedef enum lidx_status {
 #define LIDX_BF16 1
 #define LIDX_E4M3 2 /* OCP E4M3FN non-RoPE dims + E8M0 scale per 64 + bf16 RoPE dims */
 #define LIDX_F16 3  /* recognised and refused (LIDX_ERR_UNSUPPORTED), as the ds4 CUDA path refuses f16 comp KV */
+#define LIDX_E2M1 4 /* OCP E2M1 non-RoPE dims, two codes a byte + E8M0 scale per 32 + bf16 RoPE dims: pages of a
+                     * paged cache (lidx_pages); the other calls return LIDX_ERR_UNSUPPORTED for it */
 
 /*
  * Rows of a cache (index keys, compressed KV or sliding-window rows).
@@ -87,16 +89,20 @@ typedef enum lidx_status {
  * 2^(e-127) where e is the E8M0 byte scale[(d)/64] of the row; dims
  * [dim-64, dim) are the bf16 RoPE dims in `rope`.
  *
+ * For LIDX_E2M1: byte i of `data` holds the E2M1 codes of dims 2i (low
+ * nibble) and 2i+1 (high nibble), (dim-64)/2 bytes a row (`ld` in bytes),
+ * scaled by 2^(e-127) where e is the E8M0 byte scale[d/32]; `rope` as above.
+ *
  * Row j of batch entry b is row b*batch_rows + j of every plane; row r of a
  * plane starts at plane + r*ld (ld in elements of that plane).  Planes must
  * be 16-byte aligned and ld*elem_size a multiple of 16 (scale plane: any ld).
  */
 typedef struct lidx_kv {
-    int32_t dtype;        /* LIDX_F32 | LIDX_BF16 | LIDX_E4M3 */
+    int32_t dtype;        /* LIDX_F32 | LIDX_BF16 | LIDX_E4M3 (| LIDX_E2M1 in a lidx_pages) */
     int32_t dim;          /* 128 for index keys, 512 for attention rows */
-    const void *data;     /* F32: float, BF16: bf16, E4M3: uint8 codes */
-    const uint8_t *scale; /* E4M3 only: E8M0 codes, (dim-64)/64 per row */
-    const void *rope;     /* E4M3 only: bf16, 64 per row */
+    const void *data;     /* F32: float, BF16: bf16, E4M3: uint8 codes, E2M1: uint8 pairs of codes */
+    const uint8_t *scale; /* E8M0 codes: E4M3 (dim-64)/64 per row, E2M1 (dim-64)/32 per row */
+    const void *rope;     /* E4M3 and E2M1: bf16, 64 per row */
     int64_t ld;           /* elements between rows of `data` */
     int64_t ld_scale;     /* bytes between rows of `scale` */
     int64_t ld_rope;      /* elements between rows of `rope` */
@@ -365,6 +371,209 @@ typedef struct lidx_append_args {
 LIDX_API lidx_status lidx_cache_append(const lidx_append_args *args, void *ws, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Paged caches.  A pool of pages of `page_rows` rows each serves many
+ * sequences: row r of sequence b lies in page table[b*ld_table + r/page_rows],
+ * at row r % page_rows of it, so a cache grows by pages and shares them.  A
+ * table entry outside [0, n_pages) is no page: rows in it are skipped (never
+ * read or written) and set LIDX_DEV_BOUNDS where the call needs them.
+ * ------------------------------------------------------------------------ */
+typedef struct lidx_pages {
+    lidx_kv rows;         /* the pool: row r of page p is row p*page_rows + r of every plane (batch_rows unused) */
+    int32_t page_rows;    /* a power of two, 16 to 256 */
+    int32_t n_pages;      /* pages of the pool; n_pages * page_rows < 2^31 */
+    const int32_t *table; /* [B][ld_table] */
+    int64_t ld_table;     /* >= max_pages when B > 1 */
+    int32_t max_pages;    /* table entries a sequence has; max_pages * page_rows < 2^31 */
+} lidx_pages;
+
+/* ------------------------------------------------------------------------
+ * lidx_paged_append -- the paged cache's write side: new rows get their
+ * position rotation, are rounded to the storage format and written to their
+ * pages, in one pass.
+ *
+ *   x      [n][ld_x] x_dtype (LIDX_F32 | LIDX_BF16), rows of cache.rows.dim
+ *          (128 or 512) values; rows 16-byte aligned
+ *   cache  destination pool (LIDX_F32 | LIDX_BF16 | LIDX_E4M3 | LIDX_E2M1),
+ *          WRITTEN; B sequences
+ *   seq    [n] int32: the row's sequence; negative: a padding row, left out
+ *   row    [n] int32: its row of that sequence.  Two entries of one call that
+ *          name the same row leave any mix of the two there.
+ *   inv_freq [32] fp32 (optional): the last 64 dims are rotated in pairs,
+ *          pair i by the angle a = pos * inv_freq[i]:
+ *            (u, v) -> (u cos a - v sin a, u sin a + v cos a)
+ *          pairs (2i, 2i+1) of them with LIDX_ROPE_ADJACENT, (i, i+32) with
+ *          LIDX_ROPE_HALVES.  The angle is formed and reduced in 64 bits, so
+ *          far positions keep theirs.  NULL: no rotation.
+ *   pos    [n] int32 (optional): rotary positions; NULL: pos = row
+ * E4M3 rounding as in lidx_cache_append.  E2M1: per 32-element block the scale
+ * is 2^e with e the smallest integer in [-127, 127] such that the block's
+ * largest finite magnitude is <= 6 * 2^e (e = 0 for an all-zero block); codes
+ * are x / 2^e rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6, ties to
+ * the even code, larger magnitudes saturating; NaN is stored as 6 (code 7;
+ * the format has no NaN).  A destination that does not exist (row negative or
+ * beyond the table, seq >= B, no page) is skipped and sets LIDX_DEV_BOUNDS;
+ * a non-finite input of a written row sets LIDX_DEV_NAN.  Needs
+ * lidx_workspace_size(LIDX_OP_PAGED_APPEND) bytes (the status word).
+ * ------------------------------------------------------------------------ */
+#define LIDX_ROPE_ADJACENT 0
+#define LIDX_ROPE_HALVES 1
+
+typedef struct lidx_paged_append_args {
+    int32_t n, B;
+    int32_t x_dtype;
+    const void *x;
+    int64_t ld_x;
+    lidx_pages cache;
+    const int32_t *seq;
+    const int32_t *row;
+    const int32_t *pos;
+    const float *inv_freq;
+    int32_t rope_pairs; /* LIDX_ROPE_* */
+    uint32_t flags;     /* LIDX_LAUNCH_* */
+} lidx_paged_append_args;
+
+LIDX_API lidx_status lidx_paged_append(const lidx_paged_append_args *args, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * lidx_paged_read -- rows of a paged cache as the values they stand for.
+ *
+ *   out    [n][ld_out] out_dtype (LIDX_F32, or LIDX_BF16 rounded to nearest
+ *          even where the cache is F32; E4M3 and E2M1 values are bf16 values
+ *          while their block's scale keeps them in its range), 16-byte aligned
+ *   seq, row as in lidx_paged_append; an entry with seq < 0 leaves its out
+ *          row as it was, a row that does not exist reads as zeros and sets
+ *          LIDX_DEV_BOUNDS.
+ * Needs lidx_workspace_size(LIDX_OP_PAGED_READ) bytes (the status word).
+ * ------------------------------------------------------------------------ */
+typedef struct lidx_paged_read_args {
+    int32_t n, B;
+    lidx_pages cache;
+    const int32_t *seq;
+    const int32_t *row;
+    int32_t out_dtype;
+    void *out;
+    int64_t ld_out;
+    uint32_t flags; /* LIDX_LAUNCH_* */
+} lidx_paged_read_args;
+
+LIDX_API lidx_status lidx_paged_read(const lidx_paged_read_args *args, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * lidx_block_pool -- summaries of the blocks (pages) of a paged index-key
+ * cache, for lidx_block_select.  For block j of sequence b, with the rows
+ * r in [j*page_rows, min(len[b], (j+1)*page_rows)) it holds and p its page:
+ *
+ *   mean[d]     = sum_r key_r[d] / count            (64-bit sums)
+ *   scale[p]    = fp32(max_d |mean[d]| / 127)
+ *   codes[p][d] = rint(mean[d] / scale[p])          (ties to even; 0 when the
+ *                                                    scale is 0)
+ *
+ * for every block with rows, or, with `first`, those that hold a row >=
+ * first[b] (the blocks that an append touched).  Summaries are kept by page,
+ * as the rows are; the others stay as they were.  A block with a non-finite
+ * mean gets scale NaN and codes 0 (never selected by its score) and sets
+ * LIDX_DEV_NAN; lens beyond the table are cut to it and set LIDX_DEV_BOUNDS.
+ *   keys   dim 128: LIDX_F32 | LIDX_BF16 | LIDX_E4M3 | LIDX_E2M1
+ *   len    [B] int32; first [B] int32 (optional)
+ *   codes  [n_pages][128] int8, 16-byte aligned; scale [n_pages] fp32
+ * Needs lidx_workspace_size(LIDX_OP_BLOCK_POOL) bytes (the status word).
+ * ------------------------------------------------------------------------ */
+typedef struct lidx_block_pool_args {
+    int32_t B;
+    lidx_pages keys;
+    const int32_t *len;
+    const int32_t *first;
+    int8_t *codes;
+    float *scale;
+    uint32_t flags; /* LIDX_LAUNCH_* */
+} lidx_block_pool_args;
+
+LIDX_API lidx_status lidx_block_pool(const lidx_block_pool_args *args, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * lidx_block_select -- the blocks that each query attends to, by a cheap
+ * score of their summaries: the indexer's rule on 8-bit whole numbers.
+ *
+ * Query t of sequence b sees the rows r < v = len[b] - (T-1-t) (the T queries
+ * are the sequence's last T rows), so the blocks j < nb = ceil(v/page_rows).
+ *   sq[h]    = max_d |q[b,t,h,d]| / 127              (fp32)
+ *   qi[h,d]  = rint(q[b,t,h,d] * (127 / max_d |q[b,t,h,d]|))   (fp32; 0 when the head is 0)
+ *   score[j] = (sum_h (w[b,t,h] * sq[h]) * max(qi[h] . codes[p_j], 0)) * scale[p_j]
+ * with the dot products in whole numbers, w * sq rounded to fp32 and the rest
+ * in 64 bits, so that the ranking is the formula's and does not depend on the
+ * order of sums.  The first n_first and the last n_last of the nb blocks are
+ * always taken (sink and local blocks) and rank above all others; equal
+ * scores are ranked by index, lower first.  A block whose score is NaN or
+ * that has no page is never taken by its score and sets LIDX_DEV_NAN or
+ * LIDX_DEV_BOUNDS.
+ *
+ *   q      [B][T][H][128] bf16, 16-byte aligned, H <= 64;  w [B][T][H] fp32
+ *   codes, scale as lidx_block_pool writes them (summaries of n_pages pages)
+ *   ids    [B][T][k] int32: the taken blocks in ascending order, then -1
+ *   n_sel  [B][T] int32 (optional): how many were taken
+ * k in [1, 256], n_first + n_last <= k, at most 131072 blocks a sequence
+ * (larger: LIDX_ERR_UNSUPPORTED).  lens beyond the table are cut to
+ * it and set LIDX_DEV_BOUNDS.  Needs
+ * lidx_workspace_size(LIDX_OP_BLOCK_SELECT) bytes.
+ * ------------------------------------------------------------------------ */
+typedef struct lidx_block_select_args {
+    int32_t B, T, H, k;
+    int32_t n_first, n_last;
+    const void *q;
+    const float *w;
+    const int8_t *codes;
+    const float *scale;
+    int32_t page_rows, n_pages;
+    const int32_t *table;
+    int64_t ld_table;
+    int32_t max_pages;
+    const int32_t *len;
+    int32_t *ids;
+    int32_t *n_sel;
+    uint32_t flags; /* LIDX_LAUNCH_* */
+} lidx_block_select_args;
+
+LIDX_API lidx_status lidx_block_select(const lidx_block_select_args *args, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * lidx_paged_attn -- MQA attention (K = V = the full 512-wide row) of the
+ * last T tokens of B sequences over a paged cache, in 4 bits or wider.
+ *
+ *   R_bt = { rows r < len[b] - (T-1-t) }               blocks NULL
+ *        = those of them in the blocks blocks[b][t][i], i < n_b, that are
+ *          >= 0 (n_b = n_sel[b][t] if given, else n_blocks); a block named
+ *          twice counts twice
+ *   out[b,t,h,:] = sum_{r in R_bt} softmax_r(scale * q[b,t,h,:] . x_r) x_r
+ *   lse[b,t,h]   = log sum_{r in R_bt} exp(scale * q[b,t,h,:] . x_r)  (optional)
+ *
+ *   q     [B][T][H][512] bf16, 16-byte aligned, H <= 128
+ *   cache dim 512, LIDX_E2M1 | LIDX_E4M3 | LIDX_BF16
+ *   out   [B][T][H][512] bf16
+ * Rows in pages that do not exist, and blocks outside the table, are skipped
+ * and set LIDX_DEV_BOUNDS (-1 in blocks is no error); lens beyond the table
+ * are cut to it and set LIDX_DEV_BOUNDS.  Rows that are not attended to are
+ * never read, whatever they hold.  Empty R gives out = 0 and lse = -inf.
+ * Needs lidx_workspace_size(LIDX_OP_PAGED_ATTN) bytes (partial results); one
+ * workspace serves one call at a time.
+ * ------------------------------------------------------------------------ */
+typedef struct lidx_paged_attn_args {
+    int32_t B, T, H;
+    const void *q;
+    lidx_pages cache;
+    const int32_t *len;
+    const int32_t *blocks;
+    int32_t n_blocks;
+    int64_t ld_blocks; /* between queries, >= n_blocks */
+    const int32_t *n_sel;
+    float scale;
+    void *out;
+    float *lse;
+    uint32_t flags; /* LIDX_LAUNCH_* */
+} lidx_paged_attn_args;
+
+LIDX_API lidx_status lidx_paged_attn(const lidx_paged_attn_args *args, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
  * lidx_selection_eval -- selection evaluation over a tau-window.
  * `ops` is a bit mask; the requested steps run in this order:
  *
@@ -452,6 +661,11 @@ LIDX_API lidx_status lidx_selection_eval(const lidx_eval_args *args, void *ws, s
 #define LIDX_OP_EVAL 3
 #define LIDX_OP_DECODE 4
 #define LIDX_OP_APPEND 5
+#define LIDX_OP_PAGED_APPEND 6
+#define LIDX_OP_PAGED_READ 7
+#define LIDX_OP_BLOCK_POOL 8
+#define LIDX_OP_BLOCK_SELECT 9
+#define LIDX_OP_PAGED_ATTN 10
 
 /* Bytes of workspace call `op` needs for `args` (a pointer to the matching
  * *_args struct, host memory).  Score needs none (0). */
@@ -479,7 +693,8 @@ LIDX_API int lidx_abi_version(void);
 
 /* sizeof() of the argument structs as compiled into the library, for binding
  * checks: which = 0 lidx_kv, 1 score, 2 topk, 3 attn, 4 eval, 5 decode,
- * 6 append. */
+ * 6 append, 7 lidx_pages, 8 paged append, 9 paged read, 10 block pool, 11 block
+ * select, 12 paged attention. */
 LIDX_API size_t lidx_struct_size(int which);
 
 #ifdef __cplusplus

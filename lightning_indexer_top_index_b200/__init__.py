@@ -9,6 +9,9 @@ if the library is missing or the device is not sm_100, calls raise.
     scores = lidx.index_score(q, w, keys)                 # [B][Q][N]
     ids, n_sel = lidx.topk_select(scores, k=512)           # [B][Q][k]
     out, lse = lidx.sparse_attn_decode(q_attn, kv, N, ids[:, 0], n_sel[:, 0], swa, 128, scale)
+
+Paged caches (paged.py): paged_append, paged_read, block_pool, block_select
+and paged_attn.
 """
 from __future__ import annotations
 
@@ -24,8 +27,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblidx.so")
 
 # ---------------------------------------------------------------- constants
-F32, BF16, E4M3, F16 = 0, 1, 2, 3
-DTYPES = {"f32": F32, "bf16": BF16, "e4m3": E4M3, "f16": F16}
+F32, BF16, E4M3, F16, E2M1 = 0, 1, 2, 3, 4
+DTYPES = {"f32": F32, "bf16": BF16, "e4m3": E4M3, "f16": F16, "e2m1": E2M1}
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE = 0, 1, 2, 3, 4
 DEV_BOUNDS, DEV_NAN, DEV_TIMEOUT = 0x1, 0x2, 0x4
@@ -36,6 +39,8 @@ STATS_SPAN = 32  # entries per score-bounds record (optional scorer output, top-
 EVAL_GOLDEN, EVAL_TOPP, EVAL_VOTE, EVAL_LSA, EVAL_OVERLAP = 0x1, 0x2, 0x4, 0x8, 0x10
 EVAL_GOLDEN_INDEX = 0x20  # probs as the softmax of the indexer logits (the other golden reading)
 OP_SCORE, OP_TOPK, OP_ATTN, OP_EVAL, OP_DECODE, OP_APPEND = 0, 1, 2, 3, 4, 5
+OP_PAGED_APPEND, OP_PAGED_READ, OP_BLOCK_POOL, OP_BLOCK_SELECT, OP_PAGED_ATTN = 6, 7, 8, 9, 10
+ROPE_ADJACENT, ROPE_HALVES = 0, 1  # which of a row's 64 RoPE dims are rotated together
 
 # Layer schedule of DeepSeek-V4-Flash (architecture post, section (A) table):
 # layers 0-1 sliding window only, even layers 2..42 CSA (4:1 + top-k), odd
@@ -134,9 +139,47 @@ class AppendArgs(C.Structure):
                 ("capacity", C.c_int64), ("pos", C.c_void_p), ("ring", C.c_int32), ("flags", C.c_uint32)]
 
 
-_STRUCTS = [KVArgs, ScoreArgs, TopkArgs, AttnArgs, EvalArgs, DecodeArgs, AppendArgs]
+class PagesArgs(C.Structure):
+    _fields_ = [("rows", KVArgs), ("page_rows", C.c_int32), ("n_pages", C.c_int32), ("table", C.c_void_p),
+                ("ld_table", C.c_int64), ("max_pages", C.c_int32)]
+
+
+class PagedAppendArgs(C.Structure):
+    _fields_ = [("n", C.c_int32), ("B", C.c_int32), ("x_dtype", C.c_int32), ("x", C.c_void_p), ("ld_x", C.c_int64),
+                ("cache", PagesArgs), ("seq", C.c_void_p), ("row", C.c_void_p), ("pos", C.c_void_p),
+                ("inv_freq", C.c_void_p), ("rope_pairs", C.c_int32), ("flags", C.c_uint32)]
+
+
+class PagedReadArgs(C.Structure):
+    _fields_ = [("n", C.c_int32), ("B", C.c_int32), ("cache", PagesArgs), ("seq", C.c_void_p), ("row", C.c_void_p),
+                ("out_dtype", C.c_int32), ("out", C.c_void_p), ("ld_out", C.c_int64), ("flags", C.c_uint32)]
+
+
+class BlockPoolArgs(C.Structure):
+    _fields_ = [("B", C.c_int32), ("keys", PagesArgs), ("len", C.c_void_p), ("first", C.c_void_p),
+                ("codes", C.c_void_p), ("scale", C.c_void_p), ("flags", C.c_uint32)]
+
+
+class BlockSelectArgs(C.Structure):
+    _fields_ = [("B", C.c_int32), ("T", C.c_int32), ("H", C.c_int32), ("k", C.c_int32), ("n_first", C.c_int32),
+                ("n_last", C.c_int32), ("q", C.c_void_p), ("w", C.c_void_p), ("codes", C.c_void_p),
+                ("scale", C.c_void_p), ("page_rows", C.c_int32), ("n_pages", C.c_int32), ("table", C.c_void_p),
+                ("ld_table", C.c_int64), ("max_pages", C.c_int32), ("len", C.c_void_p), ("ids", C.c_void_p),
+                ("n_sel", C.c_void_p), ("flags", C.c_uint32)]
+
+
+class PagedAttnArgs(C.Structure):
+    _fields_ = [("B", C.c_int32), ("T", C.c_int32), ("H", C.c_int32), ("q", C.c_void_p), ("cache", PagesArgs),
+                ("len", C.c_void_p), ("blocks", C.c_void_p), ("n_blocks", C.c_int32), ("ld_blocks", C.c_int64),
+                ("n_sel", C.c_void_p), ("scale", C.c_float), ("out", C.c_void_p), ("lse", C.c_void_p),
+                ("flags", C.c_uint32)]
+
+
+_STRUCTS = [KVArgs, ScoreArgs, TopkArgs, AttnArgs, EvalArgs, DecodeArgs, AppendArgs, PagesArgs, PagedAppendArgs,
+            PagedReadArgs, BlockPoolArgs, BlockSelectArgs, PagedAttnArgs]
 EXPORTS = ("lidx_index_score", "lidx_topk_select", "lidx_sparse_attn_decode", "lidx_selection_eval",
-           "lidx_decode_layer", "lidx_cache_append", "lidx_workspace_size", "lidx_launch_count",
+           "lidx_decode_layer", "lidx_cache_append", "lidx_paged_append", "lidx_paged_read", "lidx_block_pool",
+           "lidx_block_select", "lidx_paged_attn", "lidx_workspace_size", "lidx_launch_count",
            "lidx_read_device_status",
            "lidx_status_string", "lidx_abi_version", "lidx_struct_size")
 
@@ -161,6 +204,11 @@ def lib():
                 ("lidx_selection_eval", I, [C.POINTER(EvalArgs), P, SZ, P]),
                 ("lidx_decode_layer", I, [C.POINTER(DecodeArgs), P, SZ, P]),
                 ("lidx_cache_append", I, [C.POINTER(AppendArgs), P, SZ, P]),
+                ("lidx_paged_append", I, [C.POINTER(PagedAppendArgs), P, SZ, P]),
+                ("lidx_paged_read", I, [C.POINTER(PagedReadArgs), P, SZ, P]),
+                ("lidx_block_pool", I, [C.POINTER(BlockPoolArgs), P, SZ, P]),
+                ("lidx_block_select", I, [C.POINTER(BlockSelectArgs), P, SZ, P]),
+                ("lidx_paged_attn", I, [C.POINTER(PagedAttnArgs), P, SZ, P]),
                 ("lidx_workspace_size", I, [I, P, C.POINTER(SZ)]),
                 ("lidx_launch_count", I, [I, P, C.POINTER(I)]),
                 ("lidx_read_device_status", I, [P, C.POINTER(C.c_uint32), P]),
@@ -203,9 +251,9 @@ def _ptr(t) -> Optional[int]:
 class DeviceKV:
     """Device-resident rows in one of the storage formats (see lidx_kv).
 
-    data:  f32 [rows][ld] | bf16 [rows][ld] | uint8 [rows][ld] (E4M3 codes)
-    scale: uint8 [rows][ld_scale] E8M0 codes (E4M3 only)
-    rope:  bf16 [rows][ld_rope] (E4M3 only)
+    data:  f32 [rows][ld] | bf16 [rows][ld] | uint8 [rows][ld] (E4M3 codes, or pairs of E2M1 codes)
+    scale: uint8 [rows][ld_scale] E8M0 codes (E4M3 and E2M1)
+    rope:  bf16 [rows][ld_rope] (E4M3 and E2M1)
     """
     dtype: int
     dim: int
@@ -486,3 +534,9 @@ def sparse_attn_decode_noalloc(q: torch.Tensor, kv: DeviceKV, N: int, ids: torch
     a = attn_args(q, kv, N, ids, n_sel, swa, swa_len, scale, out, lse)
     _check(f(C.byref(a), C.c_void_p(_ptr(dev_status)), _stream(stream)), "lidx_sparse_attn_decode_noalloc")
     return out, lse
+
+
+# paged caches (the calls on lidx_pages)
+from .paged import (PagedCall, PagedKV, PagedLayer, block_pool, block_pool_call, block_select,  # noqa: E402
+                    block_select_call, paged_append, paged_append_call, paged_attn, paged_attn_call, paged_read,
+                    paged_read_call)

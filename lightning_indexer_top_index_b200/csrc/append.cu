@@ -13,61 +13,13 @@
 // above 448, infinities included, saturate) and mapping NaN to 0x7F.  The
 // RoPE dims and bf16 caches round to nearest even.
 #include "kernels.cuh"
+#include "quant.cuh"
 
 namespace lidx {
 
 namespace {
 
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ uint32_t e4m3x2(float hi, float lo) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// E4M3 code of v already divided by its block scale: NaN -> 0x7F, |v| > 448
-// saturates, else the nearest code (ties to even).
-__device__ __forceinline__ float e4m3_prep(float v) {
-  return fabsf(v) > 448.f ? copysignf(448.f, v) : v;  // NaN compares false and stays NaN
-}
-
-__device__ __forceinline__ uint32_t pack4_e4m3(const float *v) {
-  uint32_t c[4];
-#pragma unroll
-  for (int i = 0; i < 4; i++) c[i] = is_nan_bits(v[i]) ? 0x7Fu : 0u;
-  const uint32_t lo = e4m3x2(e4m3_prep(v[1]), e4m3_prep(v[0]));
-  const uint32_t hi = e4m3x2(e4m3_prep(v[3]), e4m3_prep(v[2]));
-  uint32_t r = lo | (hi << 16);
-#pragma unroll
-  for (int i = 0; i < 4; i++)
-    if (c[i]) r = (r & ~(0xFFu << (8 * i))) | (0x7Fu << (8 * i));
-  return r;
-}
-
-// bf16 bits of x, nearest even; NaN keeps its payload's top bits, quieted
-__device__ __forceinline__ uint32_t bf16_bits(float x) {
-  const uint32_t u = __float_as_uint(x);
-  if (is_nan_bits(x)) return (u >> 16) | 0x40u;
-  return __bfloat16_as_ushort(__float2bfloat16_rn(x));
-}
-
-__device__ __forceinline__ uint4 pack8_bf16(const float *v) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; i++) w[i] = bf16_bits(v[2 * i]) | (bf16_bits(v[2 * i + 1]) << 16);
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// smallest e in [-127, 127] with amax <= 448 * 2^e (amax finite, > 0)
-__device__ __forceinline__ int block_exponent(float amax) {
-  int ex;
-  frexpf(amax, &ex);  // amax = f * 2^ex, f in [0.5, 1)
-  int e = max(-127, min(127, ex - 9));
-  while (e < 127 && amax > ldexpf(448.f, e)) e++;
-  while (e > -127 && amax <= ldexpf(448.f, e - 1)) e--;
-  return e;
-}
 
 __global__ void __launch_bounds__(kThreads) append_kernel(const lidx_append_args a, uint32_t *status) {
   const int dim = a.cache.dim;
@@ -113,7 +65,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const lidx_append_args
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
   if (a.cache.dtype == LIDX_E4M3 && d0 < dim - 64) {
-    const int e = am > 0.f ? block_exponent(am) : 0;
+    const int e = am > 0.f ? block_exponent_e4m3(am) : 0;
     const float inv = ldexpf(1.f, -e);  // exact power of two (e <= 120 for finite fp32 amax)
     float s[8];
 #pragma unroll

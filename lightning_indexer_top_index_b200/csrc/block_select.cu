@@ -1,0 +1,496 @@
+// Block selection: the cheap score of every block a query sees, and the k
+// blocks with the largest.
+//
+// Score.  A warp takes eight blocks at a time with mma.m16n8k32 (s8): the 64
+// heads' 8-bit queries are the A operand, held in registers for the whole row
+// (4 tiles of 16 heads x 4 steps of 32 dims); a block's 128 codes are the B
+// operand, loaded as 32 bytes by each of four lanes (a dot product does not
+// care which dims a step takes, so a lane's own 32 bytes are its share of all
+// four steps).  The dots are whole numbers below 2^21.  Each lane folds its 8
+// heads' ReLU'd dots with 64-bit weights and the 8 lanes of a block add up.  A
+// dot becomes a double by its bits (2^52 + n, minus 2^52), which costs an add.
+//
+// Selection.  Scores become order-preserving 64-bit keys in shared memory
+// (0: not eligible, all ones: always taken); the k-th largest is found by
+// radix over 11-bit digits from the highest bit in which the keys differ,
+// until the digit that holds it has few keys, which are ranked directly.  Ids
+// come out ascending by a prefix sum; equal keys are taken from the lowest
+// index on.
+//
+// A row's blocks are split over a cluster of up to 8 CTAs when there are few
+// rows; every CTA selects its k best, pushes them into the first CTA's shared
+// memory, and that one selects among them in the same way (the slices are
+// contiguous, so the lists stay in index order).
+#include <algorithm>
+
+#include "paged.cuh"
+#include "tc.cuh"
+
+namespace lidx {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxSlice = 16384;  // keys a CTA holds
+constexpr int kMaxK = 256;
+constexpr int kDigit = 11, kBins = 1 << kDigit;
+constexpr int kCand = 256;        // keys ranked directly
+constexpr int kPitch = 144;       // bytes between a head's codes: 16-byte reads of 8 heads x 4 lanes hit all banks
+constexpr uint64_t kForced = ~0ull;
+
+struct Smem {
+  alignas(16) uint8_t q[64 * kPitch];
+  double weight[64];
+  uint32_t hist[kBins];
+  uint64_t cand[kCand];
+  uint64_t red_or[kWarps], red_and[kWarps];
+  uint32_t scan_a[kWarps], scan_b[kWarps];
+  uint32_t n_cand, bin, above, bin_count;
+  uint64_t threshold;
+  uint32_t need;
+  // the first CTA's side of the exchange
+  uint32_t in_count[kMaxCluster];
+};
+
+__device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ double whole(int n) {  // n in [0, 2^31)
+  return __hiloint2double(0x43300000, n) - 4503599627370496.0;
+}
+
+// larger double -> larger key in [1, kForced), -0 as +0; NaN -> 0.  No finite
+// or infinite double reaches kForced (it would be a NaN).
+__device__ __forceinline__ uint64_t key_of(double s) {
+  if (s != s) return 0ull;
+  if (s == 0.) s = 0.;
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(s));
+  return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t remote(const void *p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(p)), "r"(rank));
+  return a;
+}
+
+// exclusive prefix sums of (x, y) over the CTA's threads, and the totals
+__device__ __forceinline__ void scan2(Smem &sm, uint32_t x, uint32_t y, uint32_t &px, uint32_t &py, uint32_t &tx,
+                                      uint32_t &ty) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t ix = warp_inclusive_scan(x), iy = warp_inclusive_scan(y);
+  __syncthreads();
+  if (lane == 31) {
+    sm.scan_a[warp] = ix;
+    sm.scan_b[warp] = iy;
+  }
+  __syncthreads();
+  px = ix - x;
+  py = iy - y;
+  tx = ty = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; w++) {
+    const uint32_t u = sm.scan_a[w], v = sm.scan_b[w];
+    if (w < warp) {
+      px += u;
+      py += v;
+    }
+    tx += u;
+    ty += v;
+  }
+}
+
+// The k-th largest (k >= 1) of those of the n keys that are neither 0 nor
+// kForced, of which there are `count` > k: sm.threshold, and in sm.need how
+// many keys equal to it belong to the k largest.
+__device__ __forceinline__ bool ranked(uint64_t key) { return key + 1ull > 1ull; }  // neither 0 nor kForced
+
+__device__ void kth_largest(Smem &sm, const uint64_t *keys, int n, uint32_t count, uint32_t k) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t any = 0ull, all = ~0ull;
+  for (int i = tid; i < n; i += kThreads) {
+    const uint64_t x = keys[i];
+    if (ranked(x)) {
+      any |= x;
+      all &= x;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    any |= __shfl_xor_sync(0xFFFFFFFFu, any, o);
+    all &= __shfl_xor_sync(0xFFFFFFFFu, all, o);
+  }
+  if (lane == 0) {
+    sm.red_or[warp] = any;
+    sm.red_and[warp] = all;
+  }
+  __syncthreads();
+  any = 0ull;
+  all = ~0ull;
+#pragma unroll
+  for (int w = 0; w < kWarps; w++) {
+    any |= sm.red_or[w];
+    all &= sm.red_and[w];
+  }
+  const uint64_t differ = any ^ all;
+  int top = differ ? 64 - __clzll(static_cast<long long>(differ)) : 0;  // bits [0, top) may differ
+  uint64_t prefix = top < 64 ? (all >> top) : 0ull;                     // the k-th key's bits from `top` on
+  uint32_t want = k;                                                    // its rank among the `count` keys with that prefix
+  while (top > 0 && count > kCand) {
+    const int shift = max(top - kDigit, 0), bins = 1 << (top - shift);
+    for (int i = tid; i < kBins; i += kThreads) sm.hist[i] = 0u;
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+      const uint64_t x = keys[i];
+      if (ranked(x) && (top == 64 || (x >> top) == prefix)) atomicAdd(&sm.hist[static_cast<uint32_t>(x >> shift) & (bins - 1)], 1u);
+    }
+    __syncthreads();
+    // bin holding rank `want` from above: thread t sums bins [8t', 8t' + 8) with t' counted from the top
+    const int per = kBins / kThreads;
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < per; i++) mine += sm.hist[kBins - 1 - (tid * per + i)];
+    uint32_t before, dummy, tot, dummy2;
+    scan2(sm, mine, 0u, before, dummy, tot, dummy2);
+    if (before < want && want <= before + mine) {
+      uint32_t at = before;
+      for (int i = 0; i < per; i++) {
+        const int bin = kBins - 1 - (tid * per + i);
+        const uint32_t h = sm.hist[bin];
+        if (want <= at + h) {
+          sm.bin = bin;
+          sm.above = at;
+          sm.bin_count = h;
+          break;
+        }
+        at += h;
+      }
+    }
+    __syncthreads();
+    prefix = (top == 64 ? 0ull : prefix << (top - shift)) | sm.bin;
+    want -= sm.above;
+    count = sm.bin_count;
+    top = shift;
+    __syncthreads();
+  }
+  if (top == 0) {  // every remaining key is the same
+    if (tid == 0) {
+      sm.threshold = prefix;
+      sm.need = want;
+    }
+    __syncthreads();
+    return;
+  }
+  if (tid == 0) sm.n_cand = 0u;
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads) {
+    const uint64_t x = keys[i];
+    if (ranked(x) && (top == 64 || (x >> top) == prefix)) sm.cand[atomicAdd(&sm.n_cand, 1u)] = x;
+  }
+  __syncthreads();
+  const int nc = sm.n_cand;  // == count <= kCand
+  if (tid < nc) {
+    const uint64_t x = sm.cand[tid];
+    uint32_t above = 0, same = 0;
+    for (int i = 0; i < nc; i++) {
+      above += sm.cand[i] > x;
+      same += sm.cand[i] == x;
+    }
+    if (above < want && want <= above + same) {  // all threads with this value write the same
+      sm.threshold = x;
+      sm.need = want - above;
+    }
+  }
+  __syncthreads();
+}
+
+// Calls emit(slot, i) for the k largest of keys[0..n) (ties to the lower i),
+// slots 0.. in ascending i; returns how many there are.
+template <typename Emit>
+__device__ int select_k(Smem &sm, const uint64_t *keys, int n, int k, Emit emit) {
+  const int tid = threadIdx.x;
+  uint32_t some = 0, must = 0;
+  for (int i = tid; i < n; i += kThreads) {
+    some += keys[i] != 0ull;
+    must += keys[i] == kForced;
+  }
+  uint32_t p, q, eligible, forced;
+  scan2(sm, some, must, p, q, eligible, forced);
+  const bool all = eligible <= static_cast<uint32_t>(k);
+  uint64_t T = 0ull;  // keys > T are taken, and `need` of those equal to it
+  uint32_t need = 0;
+  if (!all && forced >= static_cast<uint32_t>(k)) {
+    T = kForced;
+    need = k;
+  } else if (!all) {
+    kth_largest(sm, keys, n, eligible - forced, k - forced);
+    T = sm.threshold;
+    need = sm.need;
+  }
+  const int per = (n + kThreads - 1) / kThreads, lo = min(tid * per, n), hi = min(lo + per, n);
+  uint32_t gt = 0, eq = 0;
+  for (int i = lo; i < hi; i++) {
+    gt += keys[i] > T;
+    eq += keys[i] == T;
+  }
+  uint32_t pg, pe, tg, te;
+  scan2(sm, gt, eq, pg, pe, tg, te);
+  uint32_t slot = pg + min(pe, need);
+  for (int i = lo; i < hi; i++) {
+    const uint64_t x = keys[i];
+    if (x > T || (x == T && pe < need)) emit(static_cast<int>(slot++), i);
+    pe += x == T;
+  }
+  return static_cast<int>(all ? eligible : static_cast<uint32_t>(k));
+}
+
+// gridDim.x = G * B * T: CTA r of row bt's cluster is block bt * G + r
+__global__ void __launch_bounds__(kThreads) block_select_kernel(const lidx_block_select_args a, int G, int shift,
+                                                                 int slice_cap, uint32_t *status) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
+  uint64_t *keys = reinterpret_cast<uint64_t *>(smem_raw + sizeof(Smem));  // [slice_cap], then the exchange's lists
+  const int rank = G > 1 ? static_cast<int>(cluster_rank()) : 0;
+  uint64_t *in_key = keys + slice_cap;                               // [G * k]
+  int32_t *in_id = reinterpret_cast<int32_t *>(in_key + G * a.k);    // [G * k]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t bt = blockIdx.x / G;
+  const int b = static_cast<int>(bt / a.T), t = static_cast<int>(bt % a.T);
+  if (G > 1) cluster_arrive();
+  pdl_trigger();
+  pdl_wait();
+
+  // ---- the row's queries in 8 bits: thread (head, quarter) owns 32 dims
+  {
+    const int h = tid >> 2, c = tid & 3;
+    float v[32], top = 0.f;
+    if (h < a.H) {
+      const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + (bt * a.H + h) * 128 + 32 * c);
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const uint4 w = __ldg(src + i);
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          v[8 * i + 2 * k] = bf16x2_lo(x[k]);
+          v[8 * i + 2 * k + 1] = bf16x2_hi(x[k]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; i++) v[i] = 0.f;
+    }
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < 32; i++) {
+      top = fmaxf(top, fabsf(v[i]));
+      nan |= v[i] != v[i];
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    if (nan) top = __uint_as_float(0x7FC00000u);
+    const bool bad = __shfl_xor_sync(0xFFFFFFFFu, nan, 1) | nan;
+    if (__shfl_xor_sync(0xFFFFFFFFu, bad, 2) | bad) top = __uint_as_float(0x7FC00000u);
+    const float inv = top > 0.f ? __fdiv_rn(127.f, top) : 0.f;
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      uint32_t r = 0;
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+        r |= (static_cast<uint32_t>(__float2int_rn(__fmul_rn(v[4 * i + k], inv))) & 0xFFu) << (8 * k);
+      w[i] = r;
+    }
+    uint4 *dst = reinterpret_cast<uint4 *>(sm.q + h * kPitch + 32 * c);
+    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    if (c == 0)
+      sm.weight[h] = h < a.H ? static_cast<double>(__fmul_rn(__ldg(a.w + bt * a.H + h), __fdiv_rn(top, 127.f))) : 0.;
+  }
+  __syncthreads();
+  const int g = lane >> 2, c = lane & 3;
+  uint32_t A[4][4][4];  // [tile][step][register]
+  double weight[8];
+#pragma unroll
+  for (int m = 0; m < 4; m++) {
+#pragma unroll
+    for (int half = 0; half < 2; half++) {
+      const int h = 16 * m + 8 * half + g;
+      const uint4 *src = reinterpret_cast<const uint4 *>(sm.q + h * kPitch + 32 * c);
+      const uint4 x = src[0], y = src[1];
+      A[m][0][half] = x.x; A[m][0][2 + half] = x.y;
+      A[m][1][half] = x.z; A[m][1][2 + half] = x.w;
+      A[m][2][half] = y.x; A[m][2][2 + half] = y.y;
+      A[m][3][half] = y.z; A[m][3][2 + half] = y.w;
+      weight[2 * m + half] = sm.weight[h];
+    }
+  }
+
+  // ---- this CTA's blocks [j0, j1) of the nb that the query sees
+  const int64_t most = static_cast<int64_t>(a.max_pages) << shift;
+  const int32_t len_in = __ldg(a.len + b);
+  if (len_in > most && rank == 0 && tid == 0) raise_status(status, LIDX_DEV_BOUNDS);
+  const int64_t seen = min(static_cast<int64_t>(max(len_in, 0)), most) - (a.T - 1 - t);
+  const int nb = seen > 0 ? static_cast<int>((seen + a.page_rows - 1) >> shift) : 0;
+  const int per = ((nb + G - 1) / G + 7) & ~7;
+  const int j0 = min(rank * per, nb), j1 = min(j0 + per, nb);
+  const int32_t *table = a.table + static_cast<int64_t>(b) * a.ld_table;
+  bool no_page = false, not_a_number = false;
+  const int heads_tiles = (a.H + 15) / 16;
+  for (int j = j0 + 8 * warp; j < j1; j += 8 * kWarps) {
+    // lane (g, c) loads bytes [32 c, 32 c + 32) of block j + g
+    const int jb = j + g;
+    int32_t page = jb < j1 ? __ldg(table + jb) : -1;
+    if (page < 0 || page >= a.n_pages) {
+      no_page |= jb < j1;
+      page = -1;
+    }
+    uint4 x = make_uint4(0, 0, 0, 0), y = x;
+    float scale = 0.f;
+    if (page >= 0) {
+      const uint4 *src = reinterpret_cast<const uint4 *>(a.codes + static_cast<int64_t>(page) * 128 + 32 * c);
+      x = __ldg(src);
+      y = __ldg(src + 1);
+      scale = __ldg(a.scale + page);
+    }
+    // lane (g, c) ends with heads g, g + 8 of each tile for blocks j + 2c, j + 2c + 1
+    double s0 = 0., s1 = 0.;
+#pragma unroll
+    for (int m = 0; m < 4; m++) {
+      if (m < heads_tiles) {
+        int d[4] = {0, 0, 0, 0};
+        mma_s8(d, A[m][0], x.x, x.y);
+        mma_s8(d, A[m][1], x.z, x.w);
+        mma_s8(d, A[m][2], y.x, y.y);
+        mma_s8(d, A[m][3], y.z, y.w);
+        s0 = fma(whole(max(d[0], 0)), weight[2 * m], s0);
+        s1 = fma(whole(max(d[1], 0)), weight[2 * m], s1);
+        s0 = fma(whole(max(d[2], 0)), weight[2 * m + 1], s0);
+        s1 = fma(whole(max(d[3], 0)), weight[2 * m + 1], s1);
+      }
+    }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, o);
+      s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
+    }
+    // lane (g, 0..3) < 8: block j + lane; its sum sits in s0 / s1 of lane c = lane / 2, its scale and page in lane 4 * lane
+    const double sa = __shfl_sync(0xFFFFFFFFu, s0, (lane & 7) >> 1), sb = __shfl_sync(0xFFFFFFFFu, s1, (lane & 7) >> 1);
+    const float sc = __shfl_sync(0xFFFFFFFFu, scale, 4 * (lane & 7));
+    const int32_t pg = __shfl_sync(0xFFFFFFFFu, page, 4 * (lane & 7));
+    const int jl = j + lane;
+    if (lane < 8 && jl < j1) {
+      const double score = ((lane & 1) ? sb : sa) * static_cast<double>(sc);
+      uint64_t key = pg >= 0 ? key_of(score) : 0ull;
+      if (jl < a.n_first || jl >= nb - a.n_last) key = kForced;
+      else if (pg >= 0 && key == 0ull) not_a_number = true;
+      keys[jl - j0] = key;
+    }
+  }
+  if (no_page) raise_status(status, LIDX_DEV_BOUNDS);
+  if (not_a_number) raise_status(status, LIDX_DEV_NAN);
+  __syncthreads();
+
+  int32_t *ids = a.ids + bt * a.k;
+  int n_sel;
+  if (G == 1) {
+    n_sel = select_k(sm, keys, j1 - j0, a.k, [&](int slot, int i) { ids[slot] = i; });
+  } else {
+    cluster_wait();  // the first CTA runs: its shared memory may be written
+    const uint32_t to_key = remote(in_key + rank * a.k, 0), to_id = remote(in_id + rank * a.k, 0);
+    const int mine = select_k(sm, keys, j1 - j0, a.k, [&](int slot, int i) {
+      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to_key + 8 * slot), "l"(keys[i]) : "memory");
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to_id + 4 * slot), "r"(j0 + i) : "memory");
+    });
+    if (tid == 0)
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote(&sm.in_count[rank], 0)), "r"(mine) : "memory");
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    if (rank != 0) return;
+    // the lists close up in place, in index order (list r moves down to the end of list r - 1)
+    int n = sm.in_count[0];
+    for (int r = 1; r < G; r++) {
+      const int cnt = sm.in_count[r];
+      uint64_t key = 0;
+      int32_t id = 0;
+      if (tid < cnt) {
+        key = in_key[r * a.k + tid];
+        id = in_id[r * a.k + tid];
+      }
+      __syncthreads();
+      if (tid < cnt) {
+        in_key[n + tid] = key;
+        in_id[n + tid] = id;
+      }
+      n += cnt;
+    }
+    __syncthreads();
+    n_sel = select_k(sm, in_key, n, a.k, [&](int slot, int i) { ids[slot] = in_id[i]; });
+  }
+  for (int i = n_sel + tid; i < a.k; i += kThreads) ids[i] = -1;
+  if (tid == 0 && a.n_sel) a.n_sel[bt] = n_sel;
+}
+
+// CTAs a row is split over: so that a slice fits, and, while the rows leave
+// SMs idle, down to 256 blocks a CTA.
+int cluster_for(const lidx_block_select_args &a) {
+  int g = 1;
+  while (g < kMaxCluster && (a.max_pages > g * kMaxSlice ||
+                             (a.max_pages > g * 256 && static_cast<int64_t>(a.B) * a.T * g * 2 <= 2 * 148)))
+    g *= 2;
+  return g;
+}
+
+int slice_of(const lidx_block_select_args &a, int g) { return ((a.max_pages + g - 1) / g + 7) & ~7; }
+
+}  // namespace
+
+bool block_select_supported(const lidx_block_select_args &a) {
+  return a.k <= kMaxK && a.H <= 64 && slice_of(a, cluster_for(a)) <= kMaxSlice;
+}
+
+cudaError_t launch_block_select(const lidx_block_select_args &a, void *ws, cudaStream_t st) {
+  const int g = cluster_for(a), slice = slice_of(a, g);
+  const size_t smem = sizeof(Smem) + static_cast<size_t>(slice) * 8 + (g > 1 ? static_cast<size_t>(g) * a.k * 12 : 0);
+  cudaError_t e = cudaFuncSetAttribute(block_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(g * a.B * a.T));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (g > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = g;
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    n++;
+  }
+  if (a.flags & LIDX_LAUNCH_PDL) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    n++;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, block_select_kernel, a, g, __builtin_ctz(static_cast<unsigned>(a.page_rows)), slice,
+                            static_cast<uint32_t *>(ws));
+}
+
+}  // namespace lidx

@@ -43,6 +43,18 @@ cudaError_t launch_decode_fused(const lidx_decode_args &a, void *ws, cudaStream_
 // ---- cache write side
 cudaError_t launch_append(const lidx_append_args &a, void *ws, cudaStream_t st);
 
+// ---- paged caches
+int page_shift(const lidx_pages &c);  // log2(page_rows)
+cudaError_t launch_paged_append(const lidx_paged_append_args &a, void *ws, cudaStream_t st);
+cudaError_t launch_paged_read(const lidx_paged_read_args &a, void *ws, cudaStream_t st);
+cudaError_t launch_block_pool(const lidx_block_pool_args &a, void *ws, cudaStream_t st);
+bool block_select_supported(const lidx_block_select_args &a);
+cudaError_t launch_block_select(const lidx_block_select_args &a, void *ws, cudaStream_t st);
+bool paged_attn_supported(const lidx_paged_attn_args &a);
+size_t paged_attn_workspace(const lidx_paged_attn_args &a);
+int paged_attn_launches(const lidx_paged_attn_args &a);
+cudaError_t launch_paged_attn(const lidx_paged_attn_args &a, void *ws, cudaStream_t st);
+
 // ---- selection evaluation
 bool golden_tc_supported(const lidx_eval_args &a);
 size_t golden_tc_workspace(const lidx_eval_args &a);

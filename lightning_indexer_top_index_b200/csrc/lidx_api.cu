@@ -38,7 +38,7 @@ size_t elem_size(int dt) { return dt == LIDX_F32 ? 4 : dt == LIDX_BF16 ? 2 : 1; 
 // Layout checks of a row set; `rows_per_batch` is the largest row index used + 1
 // within one batch entry.
 lidx_status check_kv(const lidx_kv &k, int dim, int B, int64_t rows_per_batch, bool overlap_ok = false) {
-  if (k.dtype == LIDX_F16) return LIDX_ERR_UNSUPPORTED;
+  if (k.dtype == LIDX_F16 || k.dtype == LIDX_E2M1) return LIDX_ERR_UNSUPPORTED;
   if (k.dtype != LIDX_F32 && k.dtype != LIDX_BF16 && k.dtype != LIDX_E4M3) return LIDX_ERR_INVALID_ARG;
   if (k.dim != dim) return LIDX_ERR_UNSUPPORTED;
   if (!k.data) return LIDX_ERR_INVALID_ARG;
@@ -170,6 +170,94 @@ lidx_status check_append(const lidx_append_args *a) {
   return LIDX_OK;
 }
 
+bool readable(const void *p) { return p && aligned(p, 4); }
+
+// A page table of B sequences over a pool of n_pages pages.
+lidx_status check_table(int B, int page_rows, int n_pages, const int32_t *table, int64_t ld_table, int max_pages) {
+  if (page_rows < 16 || page_rows > 256 || (page_rows & (page_rows - 1))) return LIDX_ERR_INVALID_ARG;
+  if (n_pages < 1 || max_pages < 1 || !readable(table)) return LIDX_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(n_pages) * page_rows > INT32_MAX || static_cast<int64_t>(max_pages) * page_rows > INT32_MAX)
+    return LIDX_ERR_INVALID_ARG;
+  if (B > 1 && ld_table < max_pages) return LIDX_ERR_INVALID_ARG;
+  return LIDX_OK;
+}
+
+lidx_status check_pages(const lidx_pages &c, int dim, int B) {
+  const lidx_kv &k = c.rows;
+  if (k.dtype == LIDX_E2M1) {
+    if (k.dim != dim) return LIDX_ERR_UNSUPPORTED;
+    if (!k.data || !k.scale || !k.rope) return LIDX_ERR_INVALID_ARG;
+    if (k.ld < (dim - 64) / 2 || k.ld_scale < (dim - 64) / 32 || k.ld_rope < 64) return LIDX_ERR_INVALID_ARG;
+    if (!aligned(k.data, 16) || k.ld % 16 != 0 || !aligned(k.rope, 16) || (k.ld_rope * 2) % 16 != 0)
+      return LIDX_ERR_INVALID_ARG;
+  } else {
+    lidx_status s = check_kv(k, dim, 1, 0);
+    if (s != LIDX_OK) return s;
+  }
+  return check_table(B, c.page_rows, c.n_pages, c.table, c.ld_table, c.max_pages);
+}
+
+lidx_status check_paged_append(const lidx_paged_append_args *a) {
+  if (!a || !a->x || !readable(a->seq) || !readable(a->row)) return LIDX_ERR_INVALID_ARG;
+  if (a->n < 1 || a->B < 1) return LIDX_ERR_INVALID_ARG;
+  if (a->cache.rows.dim != 128 && a->cache.rows.dim != 512) return LIDX_ERR_UNSUPPORTED;
+  lidx_status s = check_pages(a->cache, a->cache.rows.dim, a->B);
+  if (s != LIDX_OK) return s;
+  if (a->x_dtype != LIDX_F32 && a->x_dtype != LIDX_BF16) return LIDX_ERR_UNSUPPORTED;
+  if (!aligned(a->x, 16) || a->ld_x < a->cache.rows.dim ||
+      (a->ld_x * static_cast<int64_t>(elem_size(a->x_dtype))) % 16 != 0)
+    return LIDX_ERR_INVALID_ARG;
+  if ((a->pos && !readable(a->pos)) || (a->inv_freq && !readable(a->inv_freq))) return LIDX_ERR_INVALID_ARG;
+  if (a->rope_pairs != LIDX_ROPE_ADJACENT && a->rope_pairs != LIDX_ROPE_HALVES) return LIDX_ERR_INVALID_ARG;
+  return LIDX_OK;
+}
+
+lidx_status check_paged_read(const lidx_paged_read_args *a) {
+  if (!a || !a->out || !readable(a->seq) || !readable(a->row)) return LIDX_ERR_INVALID_ARG;
+  if (a->n < 1 || a->B < 1) return LIDX_ERR_INVALID_ARG;
+  if (a->cache.rows.dim != 128 && a->cache.rows.dim != 512) return LIDX_ERR_UNSUPPORTED;
+  lidx_status s = check_pages(a->cache, a->cache.rows.dim, a->B);
+  if (s != LIDX_OK) return s;
+  if (a->out_dtype != LIDX_F32 && a->out_dtype != LIDX_BF16) return LIDX_ERR_UNSUPPORTED;
+  if (!aligned(a->out, 16) || a->ld_out < a->cache.rows.dim ||
+      (a->ld_out * static_cast<int64_t>(elem_size(a->out_dtype))) % 16 != 0)
+    return LIDX_ERR_INVALID_ARG;
+  return LIDX_OK;
+}
+
+lidx_status check_block_pool(const lidx_block_pool_args *a) {
+  if (!a || !readable(a->len) || (a->first && !readable(a->first))) return LIDX_ERR_INVALID_ARG;
+  if (a->B < 1 || a->B > 65535 || !a->codes || !aligned(a->codes, 16) || !readable(a->scale)) return LIDX_ERR_INVALID_ARG;
+  return check_pages(a->keys, 128, a->B);
+}
+
+lidx_status check_block_select(const lidx_block_select_args *a) {
+  if (!a || !a->q || !aligned(a->q, 16) || !readable(a->w) || !a->codes || !aligned(a->codes, 16) ||
+      !readable(a->scale) || !readable(a->len) || !readable(a->ids) || (a->n_sel && !readable(a->n_sel)))
+    return LIDX_ERR_INVALID_ARG;
+  if (a->B < 1 || a->T < 1 || a->H < 1 || a->k < 1 || a->n_first < 0 || a->n_last < 0) return LIDX_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(a->n_first) + a->n_last > a->k) return LIDX_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(a->B) * a->T > (1 << 24)) return LIDX_ERR_UNSUPPORTED;
+  lidx_status s = check_table(a->B, a->page_rows, a->n_pages, a->table, a->ld_table, a->max_pages);
+  if (s != LIDX_OK) return s;
+  return block_select_supported(*a) ? LIDX_OK : LIDX_ERR_UNSUPPORTED;
+}
+
+lidx_status check_paged_attn(const lidx_paged_attn_args *a) {
+  if (!a || !a->q || !aligned(a->q, 16) || !a->out || !aligned(a->out, 16) || !readable(a->len) ||
+      (a->lse && !readable(a->lse)))
+    return LIDX_ERR_INVALID_ARG;
+  if (a->B < 1 || a->T < 1 || a->H < 1) return LIDX_ERR_INVALID_ARG;
+  if (a->blocks && (!readable(a->blocks) || a->n_blocks < 1 || a->ld_blocks < a->n_blocks ||
+                    (a->n_sel && !readable(a->n_sel))))
+    return LIDX_ERR_INVALID_ARG;
+  if (!(a->scale == a->scale) || a->scale == INFINITY || a->scale == -INFINITY) return LIDX_ERR_INVALID_ARG;
+  lidx_status s = check_pages(a->cache, 512, a->B);
+  if (s != LIDX_OK) return s;
+  if (a->H > 128 || a->cache.rows.dtype == LIDX_F32) return LIDX_ERR_UNSUPPORTED;
+  return paged_attn_supported(*a) ? LIDX_OK : LIDX_ERR_UNSUPPORTED;
+}
+
 lidx_status check_ws(void *ws, size_t have, size_t need) {
   if (!ws || !aligned(ws, 256)) return need ? LIDX_ERR_WORKSPACE : LIDX_OK;
   return have >= need ? LIDX_OK : LIDX_ERR_WORKSPACE;
@@ -232,6 +320,46 @@ lidx_status lidx_cache_append(const lidx_append_args *args, void *ws, size_t ws_
   return from_cuda(launch_append(*args, ws, static_cast<cudaStream_t>(stream)));
 }
 
+lidx_status lidx_paged_append(const lidx_paged_append_args *args, void *ws, size_t ws_bytes, void *stream) {
+  lidx_status s = check_paged_append(args);
+  if (s != LIDX_OK) return s;
+  if ((s = check_ws(ws, ws_bytes, LIDX_WS_HEADER)) != LIDX_OK) return s;
+  if ((s = check_device()) != LIDX_OK) return s;
+  return from_cuda(launch_paged_append(*args, ws, static_cast<cudaStream_t>(stream)));
+}
+
+lidx_status lidx_paged_read(const lidx_paged_read_args *args, void *ws, size_t ws_bytes, void *stream) {
+  lidx_status s = check_paged_read(args);
+  if (s != LIDX_OK) return s;
+  if ((s = check_ws(ws, ws_bytes, LIDX_WS_HEADER)) != LIDX_OK) return s;
+  if ((s = check_device()) != LIDX_OK) return s;
+  return from_cuda(launch_paged_read(*args, ws, static_cast<cudaStream_t>(stream)));
+}
+
+lidx_status lidx_block_pool(const lidx_block_pool_args *args, void *ws, size_t ws_bytes, void *stream) {
+  lidx_status s = check_block_pool(args);
+  if (s != LIDX_OK) return s;
+  if ((s = check_ws(ws, ws_bytes, LIDX_WS_HEADER)) != LIDX_OK) return s;
+  if ((s = check_device()) != LIDX_OK) return s;
+  return from_cuda(launch_block_pool(*args, ws, static_cast<cudaStream_t>(stream)));
+}
+
+lidx_status lidx_block_select(const lidx_block_select_args *args, void *ws, size_t ws_bytes, void *stream) {
+  lidx_status s = check_block_select(args);
+  if (s != LIDX_OK) return s;
+  if ((s = check_ws(ws, ws_bytes, LIDX_WS_HEADER)) != LIDX_OK) return s;
+  if ((s = check_device()) != LIDX_OK) return s;
+  return from_cuda(launch_block_select(*args, ws, static_cast<cudaStream_t>(stream)));
+}
+
+lidx_status lidx_paged_attn(const lidx_paged_attn_args *args, void *ws, size_t ws_bytes, void *stream) {
+  lidx_status s = check_paged_attn(args);
+  if (s != LIDX_OK) return s;
+  if ((s = check_ws(ws, ws_bytes, paged_attn_workspace(*args))) != LIDX_OK) return s;
+  if ((s = check_device()) != LIDX_OK) return s;
+  return from_cuda(launch_paged_attn(*args, ws, static_cast<cudaStream_t>(stream)));
+}
+
 lidx_status lidx_workspace_size(int op, const void *args, size_t *bytes) {
   if (!args || !bytes) return LIDX_ERR_INVALID_ARG;
   lidx_status s = LIDX_OK;
@@ -259,6 +387,26 @@ lidx_status lidx_workspace_size(int op, const void *args, size_t *bytes) {
     case LIDX_OP_DECODE:
       s = check_decode(static_cast<const lidx_decode_args *>(args));
       if (s == LIDX_OK) *bytes = decode_fused_workspace(*static_cast<const lidx_decode_args *>(args));
+      break;
+    case LIDX_OP_PAGED_APPEND:
+      s = check_paged_append(static_cast<const lidx_paged_append_args *>(args));
+      if (s == LIDX_OK) *bytes = LIDX_WS_HEADER;
+      break;
+    case LIDX_OP_PAGED_READ:
+      s = check_paged_read(static_cast<const lidx_paged_read_args *>(args));
+      if (s == LIDX_OK) *bytes = LIDX_WS_HEADER;
+      break;
+    case LIDX_OP_BLOCK_POOL:
+      s = check_block_pool(static_cast<const lidx_block_pool_args *>(args));
+      if (s == LIDX_OK) *bytes = LIDX_WS_HEADER;
+      break;
+    case LIDX_OP_BLOCK_SELECT:
+      s = check_block_select(static_cast<const lidx_block_select_args *>(args));
+      if (s == LIDX_OK) *bytes = LIDX_WS_HEADER;
+      break;
+    case LIDX_OP_PAGED_ATTN:
+      s = check_paged_attn(static_cast<const lidx_paged_attn_args *>(args));
+      if (s == LIDX_OK) *bytes = paged_attn_workspace(*static_cast<const lidx_paged_attn_args *>(args));
       break;
     default:
       return LIDX_ERR_INVALID_ARG;
@@ -293,6 +441,26 @@ lidx_status lidx_launch_count(int op, const void *args, int *count) {
     case LIDX_OP_DECODE:
       s = check_decode(static_cast<const lidx_decode_args *>(args));
       if (s == LIDX_OK) *count = 1;
+      break;
+    case LIDX_OP_PAGED_APPEND:
+      s = check_paged_append(static_cast<const lidx_paged_append_args *>(args));
+      if (s == LIDX_OK) *count = 1;
+      break;
+    case LIDX_OP_PAGED_READ:
+      s = check_paged_read(static_cast<const lidx_paged_read_args *>(args));
+      if (s == LIDX_OK) *count = 1;
+      break;
+    case LIDX_OP_BLOCK_POOL:
+      s = check_block_pool(static_cast<const lidx_block_pool_args *>(args));
+      if (s == LIDX_OK) *count = 1;
+      break;
+    case LIDX_OP_BLOCK_SELECT:
+      s = check_block_select(static_cast<const lidx_block_select_args *>(args));
+      if (s == LIDX_OK) *count = 1;
+      break;
+    case LIDX_OP_PAGED_ATTN:
+      s = check_paged_attn(static_cast<const lidx_paged_attn_args *>(args));
+      if (s == LIDX_OK) *count = paged_attn_launches(*static_cast<const lidx_paged_attn_args *>(args));
       break;
     default:
       return LIDX_ERR_INVALID_ARG;
@@ -331,6 +499,12 @@ size_t lidx_struct_size(int which) {
     case 4: return sizeof(lidx_eval_args);
     case 5: return sizeof(lidx_decode_args);
     case 6: return sizeof(lidx_append_args);
+    case 7: return sizeof(lidx_pages);
+    case 8: return sizeof(lidx_paged_append_args);
+    case 9: return sizeof(lidx_paged_read_args);
+    case 10: return sizeof(lidx_block_pool_args);
+    case 11: return sizeof(lidx_block_select_args);
+    case 12: return sizeof(lidx_paged_attn_args);
   }
   return 0;
 }

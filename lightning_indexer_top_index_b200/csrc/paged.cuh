@@ -1,0 +1,105 @@
+// Paged caches on the device: from a sequence's row to its pool row, and from
+// stored rows to the values they stand for.
+#pragma once
+
+#include "kernels.cuh"
+
+namespace lidx {
+
+// Pool row of row r of sequence b, or -1 where the table has no page for it.
+// r >= 0; shift = log2(page_rows).
+__device__ __forceinline__ int32_t pool_row(const lidx_pages &c, int shift, int b, int32_t r) {
+  const int32_t j = r >> shift;
+  if (j >= c.max_pages) return -1;
+  const int32_t page = __ldg(c.table + static_cast<int64_t>(b) * c.ld_table + j);
+  if (page < 0 || page >= c.n_pages) return -1;
+  return (page << shift) | (r & (c.page_rows - 1));
+}
+
+// Rows of sequence b that exist: len cut to what the table can hold.
+__device__ __forceinline__ int32_t cut_len(int32_t len, const lidx_pages &c, bool &cut) {
+  const int32_t most = c.max_pages * c.page_rows;
+  cut = len > most;
+  return min(max(len, 0), most);
+}
+
+// E8M0 byte -> 2^(c-127) in both halves of a bf16 pair, exactly (c = 0 is the
+// bf16 subnormal 2^-127; 255 is NaN).
+__device__ __forceinline__ uint32_t e8m0_to_bf16x2(uint32_t c) {
+  const uint32_t h = c == 0u ? 0x0040u : c == 0xFFu ? 0x7FC0u : c << 7;
+  return h | (h << 16);
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Eight E2M1 codes (the first in the low nibble) -> four bf16 pairs.  The
+// magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 have the bf16 bytes
+//   low 00 00 80 C0 00 40 80 C0   high 00 3F 3F 3F 40 40 40 40,
+// which byte permutes look up with the codes themselves as selectors, four a
+// time; the sign bits are permuted into the high bytes' top bits.
+__device__ __forceinline__ void e2m1x8_to_bf16x2(uint32_t w, uint32_t (&o)[4]) {
+  const uint32_t mag = w & 0x77777777u;
+  const uint32_t even = (w << 4) & 0x80808080u, odd = w & 0x80808080u;  // signs of the low and the high nibbles
+  const uint32_t lo0 = __byte_perm(0xC0800000u, 0xC0804000u, mag);
+  const uint32_t lo1 = __byte_perm(0xC0800000u, 0xC0804000u, mag >> 16);
+  const uint32_t hi0 = __byte_perm(0x3F3F3F00u, 0x40404040u, mag) | __byte_perm(even, odd, 0x5140);
+  const uint32_t hi1 = __byte_perm(0x3F3F3F00u, 0x40404040u, mag >> 16) | __byte_perm(even, odd, 0x7362);
+  o[0] = __byte_perm(lo0, hi0, 0x5140);
+  o[1] = __byte_perm(lo0, hi0, 0x7362);
+  o[2] = __byte_perm(lo1, hi1, 0x5140);
+  o[3] = __byte_perm(lo1, hi1, 0x7362);
+}
+
+__device__ __forceinline__ float bf16x2_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16x2_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Values of dims [8t, 8t + 8) of pool row p as fp32, the exact products of
+// code and scale.
+__device__ __forceinline__ void load8(const lidx_kv &kv, int64_t p, int t, float (&v)[8]) {
+  const int d0 = 8 * t, q = kv.dim - 64;
+  if (kv.dtype == LIDX_F32) {
+    const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(kv.data) + p * kv.ld + d0);
+    const float4 a = __ldg(s), b = __ldg(s + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    return;
+  }
+  if (kv.dtype == LIDX_BF16 || d0 >= q) {
+    const uint16_t *s = kv.dtype == LIDX_BF16 ? static_cast<const uint16_t *>(kv.data) + p * kv.ld + d0
+                                              : static_cast<const uint16_t *>(kv.rope) + p * kv.ld_rope + (d0 - q);
+    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(s));
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      v[2 * i] = bf16x2_lo(x[i]);
+      v[2 * i + 1] = bf16x2_hi(x[i]);
+    }
+    return;
+  }
+  const uint8_t *data = static_cast<const uint8_t *>(kv.data);
+  uint32_t x[4];
+  float s;
+  if (kv.dtype == LIDX_E4M3) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(data + p * kv.ld + d0));
+    s = e8m0_to_f32(__ldg(kv.scale + p * kv.ld_scale + d0 / 64));
+    x[0] = e4m3x2_to_bf16x2(w.x);
+    x[1] = e4m3x2_to_bf16x2(w.x >> 16);
+    x[2] = e4m3x2_to_bf16x2(w.y);
+    x[3] = e4m3x2_to_bf16x2(w.y >> 16);
+  } else {
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(data + p * kv.ld + d0 / 2));
+    s = e8m0_to_f32(__ldg(kv.scale + p * kv.ld_scale + d0 / 32));
+    e2m1x8_to_bf16x2(w, x);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    v[2 * i] = bf16x2_lo(x[i]) * s;
+    v[2 * i + 1] = bf16x2_hi(x[i]) * s;
+  }
+}
+
+}  // namespace lidx

@@ -1,0 +1,206 @@
+// The paged cache's write side, and rows read back.
+//
+// Append: a new row's last 64 dims are rotated in pairs by the angles
+// pos * inv_freq[i], the others rounded to E4M3 or E2M1 under one power-of-two
+// scale per 64 or 32 of them, and the row goes to its page.
+//
+// A row is served by dim/16 lanes, lane t holding dims [16t, 16t + 16): a
+// whole warp for a 512-wide row, eight lanes for an index key.  The row's 32
+// angles are spread over its lanes (one, or four, each) and fetched by
+// shuffles by the four lanes that hold the rotated dims, so no lane evaluates
+// more than its share of sines.  An angle is formed as pos * inv_freq / 2 pi
+// turns in 64 bits and its whole turns dropped before it is rounded to fp32
+// (error below 2^-25 turns at any position), since in fp32 the product alone
+// would be off by up to pos * 2^-24 radians.
+#include "paged.cuh"
+#include "quant.cuh"
+
+namespace lidx {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr unsigned kAll = 0xFFFFFFFFu;
+
+__device__ __forceinline__ void load16(const void *x, int dtype, int64_t at, float (&v)[16]) {
+  if (dtype == LIDX_F32) {
+    const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(x) + at);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const float4 a = __ldg(s + i);
+      v[4 * i] = a.x; v[4 * i + 1] = a.y; v[4 * i + 2] = a.z; v[4 * i + 3] = a.w;
+    }
+  } else {
+    const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + at);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const uint4 a = __ldg(s + i);
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        v[8 * i + 2 * k] = bf16x2_lo(w[k]);
+        v[8 * i + 2 * k + 1] = bf16x2_hi(w[k]);
+      }
+    }
+  }
+}
+
+template <int kDim>
+__global__ void __launch_bounds__(kThreads) paged_append_kernel(const lidx_paged_append_args a, int shift,
+                                                                 uint32_t *status) {
+  constexpr int kLanes = kDim / 16;          // lanes of a row
+  constexpr int kAngles = 32 / kLanes;       // angles a lane evaluates
+  constexpr int kRows = kThreads / kLanes;   // rows of a block
+  const int t = threadIdx.x % kLanes, lane = threadIdx.x & 31;
+  const int base = lane - t;                 // the row's first lane
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kLanes;
+  pdl_trigger();
+  pdl_wait();  // rows, positions and tables may come from the previous kernel
+  // lanes of rows behind the last one stay for the shuffles
+  int seq = -1, row = -1, pos = 0;
+  float v[16];
+#pragma unroll
+  for (int k = 0; k < 16; k++) v[k] = 0.f;
+  if (i < a.n) {
+    seq = __ldg(a.seq + i);
+    row = __ldg(a.row + i);
+    if (a.inv_freq) pos = a.pos ? __ldg(a.pos + i) : row;
+    if (seq >= 0) load16(a.x, a.x_dtype, i * a.ld_x + 16 * t, v);
+  }
+  int32_t dst = -1;
+  if (seq >= 0) {
+    if (seq < a.B && row >= 0) dst = pool_row(a.cache, shift, seq, row);
+    if (dst < 0 && t == 0) raise_status(status, LIDX_DEV_BOUNDS);
+  }
+  bool nonfinite = false;
+#pragma unroll
+  for (int k = 0; k < 16; k++) nonfinite |= !isfinite(v[k]);
+  if (nonfinite && dst >= 0) raise_status(status, LIDX_DEV_NAN);
+
+  const int rl = t - (kLanes - 4);  // >= 0: lane rl of the four that hold the 64 RoPE dims
+  if (a.inv_freq) {
+    float cs[kAngles], sn[kAngles];
+#pragma unroll
+    for (int k = 0; k < kAngles; k++) {
+      double turns = static_cast<double>(pos) * static_cast<double>(__ldg(a.inv_freq + t * kAngles + k)) *
+                     0.15915494309189533577;
+      turns -= rint(turns);
+      sincospif(2.f * static_cast<float>(turns), &sn[k], &cs[k]);
+    }
+    const int from = rl < 0 ? 0 : rl;
+    if (a.rope_pairs == LIDX_ROPE_ADJACENT) {  // lane rl holds pairs 8 rl .. 8 rl + 7
+      float c[8], s[8];
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        // pair 8 rl + k: angle slot (8 rl + k) % kAngles of lane (8 rl + k) / kAngles
+        const int src = base + (8 * from + k) / kAngles;
+        c[k] = __shfl_sync(kAll, cs[k % kAngles], src);
+        s[k] = __shfl_sync(kAll, sn[k % kAngles], src);
+      }
+      if (rl >= 0) {
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+          const float p = v[2 * k], q = v[2 * k + 1];
+          v[2 * k] = fmaf(p, c[k], -(q * s[k]));
+          v[2 * k + 1] = fmaf(p, s[k], q * c[k]);
+        }
+      }
+    } else {  // lanes 0, 1 hold the first halves of the pairs 16 (rl & 1) .. + 15, lanes 2, 3 their second halves
+#pragma unroll
+      for (int k = 0; k < 16; k++) {
+        const int src = base + (16 * (from & 1) + k) / kAngles;
+        const float c = __shfl_sync(kAll, cs[k % kAngles], src);
+        const float s = __shfl_sync(kAll, sn[k % kAngles], src);
+        const float o = __shfl_xor_sync(kAll, v[k], 2);
+        if (rl >= 0) v[k] = rl < 2 ? fmaf(v[k], c, -(o * s)) : fmaf(o, s, v[k] * c);
+      }
+    }
+  }
+
+  // largest finite magnitude of each block: two or four neighbouring lanes
+  const int dtype = a.cache.rows.dtype;
+  float am = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; k++) {
+    const float x = fabsf(v[k]);
+    am = isfinite(x) ? fmaxf(am, x) : am;
+  }
+  am = fmaxf(am, __shfl_xor_sync(kAll, am, 1));
+  if (dtype == LIDX_E4M3) am = fmaxf(am, __shfl_xor_sync(kAll, am, 2));
+  if (dst < 0) return;
+
+  const lidx_kv &kv = a.cache.rows;
+  const int64_t p = dst;
+  if (dtype == LIDX_F32) {
+    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(const_cast<void *>(kv.data)) + p * kv.ld + 16 * t);
+#pragma unroll
+    for (int k = 0; k < 4; k++) o[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+  } else if (dtype == LIDX_BF16 || rl >= 0) {
+    uint16_t *o = dtype == LIDX_BF16 ? static_cast<uint16_t *>(const_cast<void *>(kv.data)) + p * kv.ld + 16 * t
+                                     : static_cast<uint16_t *>(const_cast<void *>(kv.rope)) + p * kv.ld_rope + 16 * rl;
+    reinterpret_cast<uint4 *>(o)[0] = pack8_bf16(v);
+    reinterpret_cast<uint4 *>(o)[1] = pack8_bf16(v + 8);
+  } else {
+    const bool e4m3 = dtype == LIDX_E4M3;
+    const int e = am > 0.f ? (e4m3 ? block_exponent_e4m3(am) : block_exponent_e2m1(am)) : 0;
+    const float inv = ldexpf(1.f, -e);  // exact: e <= 126 for a finite amax
+#pragma unroll
+    for (int k = 0; k < 16; k++) v[k] *= inv;
+    uint8_t *data = static_cast<uint8_t *>(const_cast<void *>(kv.data)) + p * kv.ld;
+    uint8_t *scale = const_cast<uint8_t *>(kv.scale) + p * kv.ld_scale;
+    if (e4m3) {
+      *reinterpret_cast<uint4 *>(data + 16 * t) =
+          make_uint4(pack4_e4m3(v), pack4_e4m3(v + 4), pack4_e4m3(v + 8), pack4_e4m3(v + 12));
+      if ((t & 3) == 0) scale[t / 4] = static_cast<uint8_t>(e + 127);
+    } else {
+      *reinterpret_cast<uint2 *>(data + 8 * t) = make_uint2(pack8_e2m1(v), pack8_e2m1(v + 8));
+      if ((t & 1) == 0) scale[t / 2] = static_cast<uint8_t>(e + 127);
+    }
+  }
+}
+
+// Rows as values: dim/8 threads a row, thread t dims [8t, 8t + 8).
+__global__ void __launch_bounds__(kThreads) paged_read_kernel(const lidx_paged_read_args a, int shift,
+                                                               uint32_t *status) {
+  const int tpr = a.cache.rows.dim / 8, t = threadIdx.x % tpr;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / tpr) + threadIdx.x / tpr;
+  pdl_trigger();
+  pdl_wait();
+  if (i >= a.n) return;
+  const int seq = __ldg(a.seq + i), row = __ldg(a.row + i);
+  if (seq < 0) return;
+  const int32_t p = seq < a.B && row >= 0 ? pool_row(a.cache, shift, seq, row) : -1;
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 8; k++) v[k] = 0.f;
+  if (p >= 0) load8(a.cache.rows, p, t, v);
+  else if (t == 0) raise_status(status, LIDX_DEV_BOUNDS);
+  if (a.out_dtype == LIDX_F32) {
+    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + i * a.ld_out + 8 * t);
+    o[0] = make_float4(v[0], v[1], v[2], v[3]);
+    o[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + i * a.ld_out + 8 * t) = pack8_bf16(v);
+  }
+}
+
+}  // namespace
+
+int page_shift(const lidx_pages &c) { return __builtin_ctz(static_cast<unsigned>(c.page_rows)); }
+
+cudaError_t launch_paged_append(const lidx_paged_append_args &a, void *ws, cudaStream_t st) {
+  const int rows = kThreads / (a.cache.rows.dim / 16);
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.n) + rows - 1) / rows));
+  auto kern = a.cache.rows.dim == 512 ? paged_append_kernel<512> : paged_append_kernel<128>;
+  return launch_kernel(kern, grid, dim3(kThreads), 0, st, (a.flags & LIDX_LAUNCH_PDL) != 0, a, page_shift(a.cache),
+                       static_cast<uint32_t *>(ws));
+}
+
+cudaError_t launch_paged_read(const lidx_paged_read_args &a, void *ws, cudaStream_t st) {
+  const int rows = kThreads / (a.cache.rows.dim / 8);
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.n) + rows - 1) / rows));
+  return launch_kernel(paged_read_kernel, grid, dim3(kThreads), 0, st, (a.flags & LIDX_LAUNCH_PDL) != 0, a,
+                       page_shift(a.cache), static_cast<uint32_t *>(ws));
+}
+
+}  // namespace lidx
