@@ -496,8 +496,9 @@ LIDX_API lidx_status lidx_block_pool(const lidx_block_pool_args *args, void *ws,
  *
  * Query t of sequence b sees the rows r < v = len[b] - (T-1-t) (the T queries
  * are the sequence's last T rows), so the blocks j < nb = ceil(v/page_rows).
- *   sq[h]    = max_d |q[b,t,h,d]| / 127              (fp32)
- *   qi[h,d]  = rint(q[b,t,h,d] * (127 / max_d |q[b,t,h,d]|))   (fp32; 0 when the head is 0)
+ *   sq[h]    = top * (1/127),                 top = max_d |q[b,t,h,d]|
+ *   qi[h,d]  = rint(q[b,t,h,d] * (127 * (1/top)))     (0 when top is 0; every
+ *              operation of these two rounded to fp32)
  *   score[j] = (sum_h (w[b,t,h] * sq[h]) * max(qi[h] . codes[p_j], 0)) * scale[p_j]
  * with the dot products in whole numbers, w * sq rounded to fp32 and the rest
  * in 64 bits, so that the ranking is the formula's and does not depend on the

@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const lidx_block
     if (nan) top = __uint_as_float(0x7FC00000u);
     const bool bad = __shfl_xor_sync(0xFFFFFFFFu, nan, 1) | nan;
     if (__shfl_xor_sync(0xFFFFFFFFu, bad, 2) | bad) top = __uint_as_float(0x7FC00000u);
-    const float inv = top > 0.f ? __fdiv_rn(127.f, top) : 0.f;
+    const float inv = top > 0.f ? __fmul_rn(__frcp_rn(top), 127.f) : 0.f;
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) {
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const lidx_block
     dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
     dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
     if (c == 0)
-      sm.weight[h] = h < a.H ? static_cast<double>(__fmul_rn(__ldg(a.w + bt * a.H + h), __fdiv_rn(top, 127.f))) : 0.;
+      sm.weight[h] = h < a.H ? static_cast<double>(__fmul_rn(__ldg(a.w + bt * a.H + h), __fmul_rn(top, 1.f / 127.f))) : 0.;
   }
   __syncthreads();
   const int g = lane >> 2, c = lane & 3;

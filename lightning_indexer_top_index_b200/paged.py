@@ -133,16 +133,17 @@ class PagedCall:
             self.launches = launch_count(op, args)
         self.ws = ws
         self._fn, self._ref = getattr(lib(), name), C.byref(args)
-        self._ws, self._bytes = C.c_void_p(ws.data_ptr()), ws.numel()
+        self._ws, self._bytes, self._index = ws.data_ptr(), ws.numel(), device.index
 
     def __call__(self, stream=None):
-        if torch.cuda.current_device() != self.device.index:
+        if torch.cuda.current_device() != self._index:
             with torch.cuda.device(self.device):
                 return self(stream)
         if stream is None:
-            stream = torch.cuda.current_stream()
-        rc = self._fn(self._ref, self._ws, self._bytes,
-                      C.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)))
+            raw = torch._C._cuda_getCurrentRawStream(self._index)
+        else:
+            raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        rc = self._fn(self._ref, self._ws, self._bytes, raw)
         if rc:
             raise LidxError(rc, self.name)
         return self.out

@@ -122,9 +122,9 @@ def select(q, w, codes, scale, table, page_rows, n_pages, length, k, n_first, n_
             if nb == 0:
                 continue
             top = np.abs(q[b, t]).max(1).astype(np.float32)
-            inv = np.where(top > 0, np.float32(127) / np.where(top > 0, top, np.float32(1)), np.float32(0)).astype(np.float32)
+            inv = np.where(top > 0, np.float32(127) * (np.float32(1) / np.where(top > 0, top, np.float32(1))), np.float32(0))
             qi = np.rint(q[b, t].astype(np.float32) * inv[:, None]).astype(np.int64)
-            weight = (w[b, t].astype(np.float32) * (top / np.float32(127)).astype(np.float32)).astype(np.float32).astype(np.float64)
+            weight = (w[b, t].astype(np.float32) * (top * (np.float32(1) / np.float32(127)))).astype(np.float32).astype(np.float64)
             pages = table[b, :nb]
             ok = (pages >= 0) & (pages < n_pages)
             p = np.where(ok, pages, 0)
