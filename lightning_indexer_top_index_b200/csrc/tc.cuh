@@ -235,4 +235,9 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn_major 
 bool make_tmap_2d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint64_t inner, uint64_t rows,
                   uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz);
 
+// 3-D tensor map over a dense [planes][rows][inner] tensor of 16-bit elements,
+// boxes of one plane; rows and planes beyond the tensor read as zeros.
+bool make_tmap_3d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint64_t inner, uint64_t rows,
+                  uint64_t planes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz);
+
 }  // namespace lidx
