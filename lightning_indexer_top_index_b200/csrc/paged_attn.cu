@@ -8,25 +8,33 @@
 // job may span CTAs.  A job that one CTA holds whole is written out by it; the
 // others leave partial results (m, l, O) that the merge kernel joins.
 //
-// A chunk, in a CTA of 13 warps:
+// A CTA has 14 warps:
+//   * the scout finds each chunk's pool rows (block list, page table) up to
+//     four chunks ahead and says where a job begins and ends;
 //   * eight loader warps, one per 64-dim slab of the row, fetch the stored
-//     rows one to two chunks ahead into registers, expand them to bf16 (exact:
-//     every E2M1 or E4M3 value times a power of two is a bf16 value) and store
-//     them as the swizzled K-major tile X[64 rows][512], two of which are in
-//     shared memory.  Rows that are not attended to are stored as zeros.
+//     rows a chunk ahead into registers, expand them to bf16 (exact: every
+//     E2M1 or E4M3 value times a power of two is a bf16 value) and store them
+//     as the swizzled K-major tile X[64 rows][512], two of which are in shared
+//     memory.  Rows that are not attended to are stored as zeros;
 //   * one thread issues S[head][row] = Q . X^T (M = 64, N = 64, K = 512) and,
 //     when the chunk's probabilities are there, O^T[d][head] += X^T . P^T
 //     (M = 128 four times, N = 64, K = 64), both on tcgen05 with fp32
-//     accumulators in TMEM; S is double buffered, so the S of a chunk runs
-//     while the softmax of the one before it does.
+//     accumulators in TMEM.  Products that add to the same accumulator wait
+//     for one another, so S is summed in four parts (K quarters) and O's four
+//     dim tiles are taken in turn;
 //   * four softmax warps read S in the 16x256b shape, in which the 32 lanes of
 //     a warp share the 16 heads of its TMEM quarter (8 head pairs x 4 column
-//     groups), so row maxima take two shuffles and no lane idles.  The running
-//     maximum moves only when it rises by more than 8 (base 2); then the O so
-//     far is rescaled in TMEM.  Sums are of the fp32 probabilities.
+//     groups), so row maxima take two shuffles and no lane idles.  S is free
+//     for the next chunk as soon as it is read.  The running maximum moves
+//     only when it rises by more than 8 (base 2); then the O so far is
+//     rescaled in TMEM.  Sums are of the fp32 probabilities.
 //   P is rounded to bf16 for the second product: 2^-9 of each probability,
 //   independent errors that average out to less than the bf16 output's own
 //   rounding.
+//
+// The loops are kept small (one place each for a product, a load, a store):
+// unrolled over their chunks they outgrew the instruction cache, and the
+// kernel spent half its time fetching code (a chunk took 8000 cycles).
 #include <algorithm>
 
 #include "paged.cuh"
@@ -42,31 +50,47 @@ constexpr int kH = 64;                   // heads of a job
 constexpr int kRows = 64;                // rows of a chunk
 constexpr int kLoaders = 8;              // warps; warp i of them fills dims [64 i, 64 i + 64)
 constexpr int kSoftmaxWarps = 4;
-constexpr int kThreads = 32 * (kSoftmaxWarps + kLoaders + 1);
+constexpr int kThreads = 32 * (kSoftmaxWarps + kLoaders + 2);
+constexpr int kMma = kSoftmaxWarps + kLoaders, kScout = kMma + 1;  // their warps
+constexpr int kRing = 4;                 // chunks the scout may be ahead
 constexpr int kPanel = 64 * 128;         // one 64-line panel of X or Q: 64 dims
 constexpr int kXBytes = 8 * kPanel;
 constexpr int kQBytes = 8 * kPanel;
 constexpr int kPBytes = kH * kRows * 2;
-constexpr uint32_t kSCol = 0;            // S buffer i at columns 64 i
-constexpr uint32_t kOCol = 128;          // O^T tile t at columns kOCol + 64 t
+constexpr int kParts = 4;                // partial sums of S, at columns 64 i
+constexpr uint32_t kOCol = 64 * kParts;  // O^T tile t at columns kOCol + 64 t
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;             // base-2 headroom of the reference maximum
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 128;
+constexpr int kFewPartials = 8;          // up to as many are joined by one thread a dim
+constexpr int kBatch = 8;                // partials whose loads are in flight together
 constexpr int kMaxCtas = 256;            // one CTA per SM
 
-struct __align__(8) Smem {
+// What the scout says about a chunk.
+constexpr uint32_t kFirst = 1u;  // the first chunk of its job in this CTA
+constexpr uint32_t kLast = 2u;   // the last one
+constexpr uint32_t kWhole = 4u;  // ... and the CTA holds all of the job's chunks
+struct __align__(16) Chunk {
+  int32_t row[kRows];  // pool rows; -1: not attended to
+  uint32_t valid[2];   // bit r: row r is attended to
+  int32_t job;
+  uint32_t flags;
+};
+
+struct __align__(16) Smem {
+  Chunk ring[kRing];
+  uint64_t ring_full[kRing], ring_free[kRing];
   uint64_t q_full;
   uint64_t x_full[2], x_free[2];  // a stage's rows are in / its second product is done (X and P free again)
-  uint64_t s_full[2], s_free[2];
+  uint64_t s_full, s_free;
   uint64_t p_full[2];
   uint64_t o_free;                // the finished job's O has been read
   uint64_t drained;               // every product issued is done (only after a wait gave up)
-  uint64_t valid[2];              // bit r: row r of the stage's chunk is attended to
   uint32_t tmem_base;
   uint32_t abort;
   float alpha[2][kH];             // rescale factors of a chunk
-  float m[kH], l[kH];
+  float l[kH];
   // the CTA's first chunk
   int32_t job, chunk;
   int32_t scan[kThreads / 32];
@@ -115,19 +139,16 @@ __device__ __forceinline__ int32_t job_chunks(const lidx_paged_attn_args &a, int
   return (job_rows(a, job, groups, shift) + kRows - 1) / kRows;
 }
 
-// Walks the CTA's chunks: `left` of them from chunk c of job on.
-struct Cursor {
-  int32_t job, c, n, left;  // n: chunks of the job
-  __device__ __forceinline__ void next(const lidx_paged_attn_args &a, int groups, int shift) {
-    left--;
-    if (++c < n) return;
-    c = 0;
-    while (left > 0) {
-      n = job_chunks(a, ++job, groups, shift);
-      if (n > 0) return;
-    }
+// tc::mbar_wait with its loop kept rolled.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile uint32_t *abort) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < tc::kWaitLimit; i++) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
   }
-};
+  *abort = 1u;
+  return false;
+}
 
 __device__ __forceinline__ float exp2_approx(float x) {  // 2 ulp; 2^-inf = 0
   float r;
@@ -195,25 +216,23 @@ struct Fmt {
   static constexpr int kRowsPerIter = 32 / kPieces;
 };
 
-// One 64-dim slab of a chunk in registers: piece it of a lane is piece
-// lane % kPieces of row it * kRowsPerIter + lane / kPieces.
+// One 64-dim slab of a chunk (or kIters * kRowsPerIter rows of it, from row
+// `from` on) in registers: piece it of a lane is piece lane % kPieces of row
+// from + it * kRowsPerIter + lane / kPieces.
 template <int kFmt, int kIters = Fmt<kFmt>::kIters>
 struct Slab {
   uint4 v[kIters];
   uint32_t scale[kFmt == LIDX_BF16 ? 1 : kIters];
 
-  // pool rows of rows lane and lane + 32 of the chunk are p0 and p1 (-1: none);
-  // `from`: first row, for a part of a chunk (kIters < Fmt::kIters)
+  // rows: the chunk's pool rows in shared memory
   __device__ __forceinline__ void load(const void *plane, int64_t ld, const uint8_t *scales, int64_t ld_scale, int slab,
-                                       int lane, int32_t p0, int32_t p1, int from) {
+                                       int lane, const int32_t *rows, int from) {
     using F = Fmt<kFmt>;
     const uint8_t *base = static_cast<const uint8_t *>(plane) + slab * (F::kPieces * 16) + (lane % F::kPieces) * 16;
     const int64_t pitch = kFmt == LIDX_BF16 ? 2 * ld : ld;
 #pragma unroll
     for (int it = 0; it < kIters; it++) {
-      const int r = from + it * F::kRowsPerIter + lane / F::kPieces;
-      const int32_t a0 = __shfl_sync(0xFFFFFFFFu, p0, r & 31), a1 = __shfl_sync(0xFFFFFFFFu, p1, r & 31);
-      const int32_t p = r < 32 ? a0 : a1;
+      const int32_t p = rows[from + it * F::kRowsPerIter + lane / F::kPieces];
       v[it] = make_uint4(0, 0, 0, 0);
       if (kFmt != LIDX_BF16) scale[it] = 127u;
       if (p >= 0) {
@@ -292,13 +311,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     tc::mbar_init(&sm->q_full, 1);
 #pragma unroll
+    for (int i = 0; i < kRing; i++) {
+      tc::mbar_init(&sm->ring_full[i], 1);
+      tc::mbar_init(&sm->ring_free[i], kSoftmaxWarps + kLoaders + 1);
+    }
+#pragma unroll
     for (int i = 0; i < 2; i++) {
       tc::mbar_init(&sm->x_full[i], kLoaders);
       tc::mbar_init(&sm->x_free[i], 1);
-      tc::mbar_init(&sm->s_full[i], 1);
-      tc::mbar_init(&sm->s_free[i], kSoftmaxWarps);
       tc::mbar_init(&sm->p_full[i], kSoftmaxWarps);
     }
+    tc::mbar_init(&sm->s_full, 1);
+    tc::mbar_init(&sm->s_free, kSoftmaxWarps);
     tc::mbar_init(&sm->o_free, kSoftmaxWarps);
     tc::mbar_init(&sm->drained, 1);
     sm->abort = 0;
@@ -319,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per = (jobs.n + kThreads - 1) / kThreads;
     const int j0 = min(tid * per, jobs.n), j1 = min(j0 + per, jobs.n);
     int32_t mine = 0;
+#pragma unroll 1
     for (int j = j0; j < j1; j++) mine += job_chunks(a, j, groups, shift);
     const int32_t incl = warp_inclusive_scan(mine);
     if (lane == 31) sm->scan[warp] = incl;
@@ -335,182 +360,207 @@ __global__ void __launch_bounds__(kThreads, 1)
     my1 = range_start(blockIdx.x + 1, jobs.G, total);
     if (before <= my0 && my0 < before + mine) {
       int32_t at = before;
+#pragma unroll 1
       for (int j = j0; j < j1; j++) {
-        const int32_t n = job_chunks(a, j, groups, shift);
-        if (at <= my0 && my0 < at + n) {
+        const int32_t m = job_chunks(a, j, groups, shift);
+        if (at <= my0 && my0 < at + m) {
           sm->job = j;
           sm->chunk = my0 - at;
         }
-        at += n;
+        at += m;
       }
     }
     __syncthreads();
   }
-  Cursor cur;
-  cur.left = my1 - my0;
-  if (cur.left > 0) {
-    cur.job = sm->job;
-    cur.c = sm->chunk;
-    cur.n = job_chunks(a, cur.job, groups, shift);
-  }
-  if (tid == 0) {
-    const int32_t start = my0 - (cur.left > 0 ? cur.c : 0);
-    const bool second =
-        cur.left > 0 && cur.c > 0 && range_start(owner(my0 - 1, jobs.G, total), jobs.G, total) <= start;
-    Split sp;
-    sp.job = second ? cur.job : -1;
-    sp.start = start;
-    sp.end = start + (second ? cur.n : 0);
-    sp.total = total;
-    ws.split[blockIdx.x] = sp;
-  }
+  const int n = my1 - my0;  // this CTA's chunks
+  auto warp_wait = [&](uint64_t *bar, uint32_t parity) {  // lane 0 waits; its view becomes the warp's
+    bool in = true;
+    if (lane == 0) in = wait_for(bar, parity, abort_flag);
+    in = __shfl_sync(0xFFFFFFFFu, in, 0);
+    __syncwarp();
+    return in;
+  };
 
-  if (cur.left > 0 && warp >= kSoftmaxWarps && warp < kSoftmaxWarps + kLoaders) {
+  if (warp == kScout) {
+    // -------------------------------------------------------------- scout
+    int32_t job = 0, c = 0, left = 0, seen = 0, rows = 0;  // `left` chunks of the job from chunk c on
+    bool bounds = false, whole = false;
+    if (n > 0) {
+      job = sm->job;
+      c = sm->chunk;
+    }
+    if (lane == 0) {  // does a job that began in the CTA before continue here, and is this its second CTA?
+      Split sp;
+      sp.job = -1;
+      sp.start = my0 - c;
+      sp.end = 0;
+      sp.total = total;
+      if (c > 0 && range_start(owner(my0 - 1, jobs.G, total), jobs.G, total) <= sp.start) {
+        sp.job = job;
+        sp.end = sp.start + (job_rows(a, job, groups, shift) + kRows - 1) / kRows;
+      }
+      ws.split[blockIdx.x] = sp;
+    }
+    for (int i = 0; i < n; i++) {
+      uint32_t flags = 0u;
+      if (left == 0) {  // a job begins: the CTA's first, or the next one with rows
+        if (i > 0) {
+          job++;
+          c = 0;
+        }
+        while ((rows = job_rows(a, job, groups, shift)) == 0) job++;
+        left = (rows + kRows - 1) / kRows - c;
+        const int32_t bt = job / groups;
+        bool cut;
+        seen = cut_len(__ldg(a.len + bt / a.T), a.cache, cut) - (a.T - 1 - bt % a.T);
+        bounds |= cut;
+        whole = c == 0;
+        flags = kFirst;
+      }
+      if (left == 1 || i + 1 == n) flags |= kLast | (whole && left == 1 ? kWhole : 0u);
+      const int32_t bt = job / groups;
+      const int32_t p0 = entry_row(a, bt, shift, c * kRows + lane, seen, rows, bounds);
+      const int32_t p1 = entry_row(a, bt, shift, c * kRows + 32 + lane, seen, rows, bounds);
+      const uint32_t v0 = __ballot_sync(0xFFFFFFFFu, p0 >= 0), v1 = __ballot_sync(0xFFFFFFFFu, p1 >= 0);
+      const int slot = i % kRing;
+      if (i >= kRing && !warp_wait(&sm->ring_free[slot], (i / kRing - 1) & 1)) break;
+      Chunk &k = sm->ring[slot];
+      k.row[lane] = p0;
+      k.row[lane + 32] = p1;
+      if (lane == 0) {
+        k.valid[0] = v0;
+        k.valid[1] = v1;
+        k.job = job;
+        k.flags = flags;
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm->ring_full[slot]);
+      c++;
+      left--;
+    }
+    if (bounds) raise_status(ws.status, LIDX_DEV_BOUNDS);
+  } else if (warp >= kSoftmaxWarps && warp < kMma) {
     // ------------------------------------------------------------ loaders
     const int slab = warp - kSoftmaxWarps;
     const lidx_kv &kv = a.cache.rows;
     constexpr bool kQuant = kFmt != LIDX_BF16;
-    constexpr int kSets = kQuant ? 2 : 1;  // chunks in registers
-    // rows of the chunk after the ones in registers
-    bool bounds = false;
-    int32_t last_job = -1, seen = 0, n_list = 0;
-    auto find_rows = [&](const Cursor &k, int32_t &p0, int32_t &p1) {
-      p0 = p1 = -1;
-      if (k.left <= 0) return;
-      const int32_t bt = k.job / groups;
-      if (k.job != last_job) {
-        last_job = k.job;
-        bool cut;
-        seen = cut_len(__ldg(a.len + bt / a.T), a.cache, cut) - (a.T - 1 - bt % a.T);
-        bounds |= cut;
-        n_list = job_rows(a, k.job, groups, shift);
-      }
-      p0 = entry_row(a, bt, shift, k.c * kRows + lane, seen, n_list, bounds);
-      p1 = entry_row(a, bt, shift, k.c * kRows + 32 + lane, seen, n_list, bounds);
-    };
-    Slab<kFmt> body[kSets];
-    Slab<LIDX_BF16, 2> rope[kSets];  // the quantised formats' RoPE dims: eight rows a warp
-    uint64_t mask[kSets];
-    auto load = [&](int set, int32_t p0, int32_t p1) {
-      if (!kQuant || slab < 7) body[set].load(kv.data, kv.ld, kv.scale, kv.ld_scale, slab, lane, p0, p1, 0);
-      if (kQuant) rope[set].load(kv.rope, kv.ld_rope, nullptr, 0, 0, lane, p0, p1, 8 * slab);
-      mask[set] = static_cast<uint64_t>(__ballot_sync(0xFFFFFFFFu, p0 >= 0)) |
-                  (static_cast<uint64_t>(__ballot_sync(0xFFFFFFFFu, p1 >= 0)) << 32);
-    };
-    const int n = cur.left;
-    Cursor ahead = cur;
-    int32_t p0, p1;
-#pragma unroll
-    for (int s = 0; s < kSets; s++) {
-      find_rows(ahead, p0, p1);
-      load(s, p0, p1);
-      if (ahead.left > 0) ahead.next(a, groups, shift);
-    }
-    find_rows(ahead, p0, p1);
-    auto step = [&](int i, int set) {
-      const int stage = i & 1;
-      bool ok = true;
-      if (i >= 2) {
-        if (lane == 0) ok = tc::mbar_wait(&sm->x_free[stage], ((i >> 1) - 1) & 1, abort_flag);
-        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    Slab<kFmt> part;
+    Slab<LIDX_BF16, 2> rope;  // the quantised formats' RoPE dims: eight rows a warp
+#pragma unroll 1
+    for (int i = 0; i <= n; i++) {  // chunk i - 1 into shared memory, chunk i into registers
+      if (i > 0) {
+        const int stage = (i - 1) & 1;
+        if (i > 2 && !warp_wait(&sm->x_free[stage], (((i - 1) >> 1) - 1) & 1)) break;
+        uint8_t *x = sX + stage * kXBytes;
+        if (!kQuant || slab < 7) part.store(x + slab * kPanel, lane, 0);
+        if (kQuant) rope.store(x + 7 * kPanel, lane, 8 * slab);
+        tc::fence_proxy_async_smem();
         __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm->x_full[stage]);
       }
-      if (!ok) return false;
-      uint8_t *x = sX + stage * kXBytes;
-      if (!kQuant || slab < 7) body[set].store(x + slab * kPanel, lane, 0);
-      if (kQuant) rope[set].store(x + 7 * kPanel, lane, 8 * slab);
-      if (slab == 0 && lane == 0) sm->valid[stage] = mask[set];
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm->x_full[stage]);
-      load(set, p0, p1);
-      if (ahead.left > 0) ahead.next(a, groups, shift);
-      find_rows(ahead, p0, p1);
-      return true;
-    };
-    for (int i = 0; i < n; i += kSets) {
-      if (!step(i, 0)) break;
-      if (kSets == 2 && i + 1 < n && !step(i + 1, kSets - 1)) break;
+      if (i < n) {
+        const int slot = i % kRing;
+        if (!warp_wait(&sm->ring_full[slot], (i / kRing) & 1)) break;
+        const int32_t *rows = sm->ring[slot].row;
+        if (!kQuant || slab < 7) part.load(kv.data, kv.ld, kv.scale, kv.ld_scale, slab, lane, rows, 0);
+        if (kQuant) rope.load(kv.rope, kv.ld_rope, nullptr, 0, 0, lane, rows, 8 * slab);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm->ring_free[slot]);
+      }
     }
-    if (bounds && slab == 0) raise_status(ws.status, LIDX_DEV_BOUNDS);
-  } else if (cur.left > 0 && warp == kSoftmaxWarps + kLoaders) {
+  } else if (warp == kMma) {
     // ------------------------------------------------- the matrix products
     if (lane == 0) {
-      const uint32_t qs = tc::smem_u32(sQ);
       const uint32_t idesc_s = tc::idesc_bf16(64, 64), idesc_o = tc::idesc_bf16(128, 64, true, false);
-      const int n = cur.left;
-      int job_no = 0;           // jobs begun so far
-      int q_loads = 0;
-      bool pending = false;     // the second product of chunk i - 1 is still to be issued
-      bool pending_first = false;
+      const uint64_t q_desc = tc::desc_kmajor_sw128(tc::smem_u32(sQ));
+      const uint64_t x_desc = tc::desc_kmajor_sw128(tc::smem_u32(sX));
+      const uint64_t xt_desc = tc::desc_mnmajor_sw128(tc::smem_u32(sX), kPanel, 1024);
+      const uint64_t p_desc = tc::desc_kmajor_sw128(tc::smem_u32(sP));
+      int begun = 0, q_loads = 0;  // jobs begun, up to chunk i
+      uint32_t flags = 0u;
       bool ok = true;
-      auto second = [&](int i, bool first) {  // O^T (+)= X^T . P^T of chunk i
-        const int stage = i & 1;
-        if (first && job_no > 1) ok = ok && tc::mbar_wait(&sm->o_free, (job_no - 2) & 1, abort_flag);
-        ok = ok && tc::mbar_wait(&sm->p_full[stage], (i >> 1) & 1, abort_flag);
-        if (!ok) return;
-        tc::tc_fence_after();
-        const uint32_t xs = tc::smem_u32(sX + stage * kXBytes), ps = tc::smem_u32(sP + stage * kPBytes);
-#pragma unroll
-        for (int dt = 0; dt < 4; dt++)
-#pragma unroll
-          for (int kk = 0; kk < kRows / 16; kk++)
-            tc::mma_bf16(tmem + kOCol + 64 * dt, tc::desc_mnmajor_sw128(xs + 2 * dt * kPanel + kk * 2048, kPanel, 1024),
-                         tc::desc_kmajor_sw128(ps + kk * 32), idesc_o, !first || kk > 0);
-        tc::mma_commit(&sm->x_free[stage]);
-      };
-      for (int i = 0; i < n && ok; i++) {
-        const int stage = i & 1;
-        const bool first = i == 0 || cur.c == 0;
-        if (first) {
-          // the last job's S products have read Q
-          if (i > 0) ok = ok && tc::mbar_wait(&sm->s_full[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag);
-          if (ok) {
+#pragma unroll 1
+      for (int i = 0; i <= n && ok; i++) {  // S of chunk i, O of chunk i - 1
+        const bool prev_first = flags & kFirst;
+        const int prev_begun = begun;
+        if (i < n) {
+          const int slot = i % kRing;
+          ok = wait_for(&sm->ring_full[slot], (i / kRing) & 1, abort_flag);
+          if (!ok) break;
+          flags = sm->ring[slot].flags;
+          const int32_t job = sm->ring[slot].job;
+          tc::mbar_arrive(&sm->ring_free[slot]);
+          if (flags & kFirst) {
+            begun++;
+            if (i > 0) ok = wait_for(&sm->s_full, (i - 1) & 1, abort_flag);  // Q has been read for the last time
+            if (!ok) break;
             tc::mbar_arrive_expect_tx(&sm->q_full, kQBytes);
             q_loads++;
-#pragma unroll
+#pragma unroll 1
             for (int p = 0; p < 8; p++)
-              tma_load_3d(sQ + p * kPanel, &tm_q, &sm->q_full, 64 * p, (cur.job % groups) * kH, cur.job / groups);
+              tma_load_3d(sQ + p * kPanel, &tm_q, &sm->q_full, 64 * p, (job % groups) * kH, job / groups);
           }
-          if (pending) second(i - 1, pending_first);
-          pending = false;
-          ok = ok && tc::mbar_wait(&sm->q_full, job_no & 1, abort_flag);
-          job_no++;
         }
-        ok = ok && tc::mbar_wait(&sm->x_full[stage], (i >> 1) & 1, abort_flag);
-        if (i >= 2) ok = ok && tc::mbar_wait(&sm->s_free[stage], ((i >> 1) - 1) & 1, abort_flag);
-        if (!ok) break;
-        tc::tc_fence_after();
-        const uint32_t xs = tc::smem_u32(sX + stage * kXBytes);
+        // S first, so that it runs while the softmax of chunk i - 1 does; where it waits for a new Q, O first
+        const int s_at = (i < n && (flags & kFirst)) ? 1 : 0;
+#pragma unroll 1
+        for (int half = 0; half < 2 && ok; half++) {
+          if (half == s_at) {
+            if (i == n) continue;
+            const int stage = i & 1;
+            if (flags & kFirst) ok = wait_for(&sm->q_full, (begun - 1) & 1, abort_flag);
+            ok = ok && wait_for(&sm->x_full[stage], (i >> 1) & 1, abort_flag);
+            if (i > 0) ok = ok && wait_for(&sm->s_free, (i - 1) & 1, abort_flag);
+            if (!ok) break;
+            tc::tc_fence_after();
+            // step k: panel k / 4, 32 bytes (k % 4) into it; part p sums panels 2p and 2p + 1
+            const uint64_t xd = x_desc + stage * (kXBytes >> 4);
+#pragma unroll 1
+            for (int j = 0; j < 8; j++) {
 #pragma unroll
-        for (int k = 0; k < kD / 16; k++) {
-          const uint32_t off = (k >> 2) * kPanel + (k & 3) * 32;
-          tc::mma_bf16(tmem + kSCol + 64 * stage, tc::desc_kmajor_sw128(qs + off), tc::desc_kmajor_sw128(xs + off),
-                       idesc_s, k > 0);
+              for (int part = 0; part < kParts; part++) {
+                const uint32_t off = (2 * part + (j >> 2)) * (kPanel >> 4) + (j & 3) * 2;
+                tc::mma_bf16(tmem + 64 * part, q_desc + off, xd + off, idesc_s, j > 0);
+              }
+            }
+            tc::mma_commit(&sm->s_full);
+          } else {
+            if (i == 0) continue;
+            const int stage = (i - 1) & 1;
+            if (prev_first && prev_begun > 1) ok = wait_for(&sm->o_free, prev_begun & 1, abort_flag);
+            ok = ok && wait_for(&sm->p_full[stage], ((i - 1) >> 1) & 1, abort_flag);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const uint64_t xd = xt_desc + stage * (kXBytes >> 4), pd = p_desc + stage * (kPBytes >> 4);
+#pragma unroll 1
+            for (int kk = 0; kk < kRows / 16; kk++) {
+#pragma unroll
+              for (int dt = 0; dt < 4; dt++)
+                tc::mma_bf16(tmem + kOCol + 64 * dt, xd + ((2 * dt * kPanel + kk * 2048) >> 4), pd + kk * 2, idesc_o,
+                             !prev_first || kk > 0);
+            }
+            tc::mma_commit(&sm->x_free[stage]);
+          }
         }
-        tc::mma_commit(&sm->s_full[stage]);
-        if (pending) second(i - 1, pending_first);
-        pending = true;
-        pending_first = first;
-        cur.next(a, groups, shift);
       }
-      if (pending && ok) second(n - 1, pending_first);
       // a wait that gave up may leave copies and products in flight: they end before the CTA does
       if (!ok) {
         volatile uint32_t unused = 0;
-        if (q_loads > 0) tc::mbar_wait(&sm->q_full, (q_loads - 1) & 1, &unused);
+        if (q_loads > 0) wait_for(&sm->q_full, (q_loads - 1) & 1, &unused);
         tc::mma_commit(&sm->drained);
-        tc::mbar_wait(&sm->drained, 0, &unused);
+        wait_for(&sm->drained, 0, &unused);
       }
     }
-  } else if (warp < kSoftmaxWarps) {
+  } else {
     // ------------------------------------------------------------ softmax
     // first, while the first rows are on their way: the jobs without rows, dealt out to the CTAs
+#pragma unroll 1
     for (int32_t j = blockIdx.x; j < jobs.n; j += jobs.G) {
       if (job_rows(a, j, groups, shift) > 0) continue;
       const int32_t bt = j / groups, g = j % groups, heads = min(kH, a.H - g * kH);
       const int64_t row = static_cast<int64_t>(bt) * a.H + g * kH;
       uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + row * kD);
+#pragma unroll 1
       for (int i = tid; i < heads * kD / 8; i += 32 * kSoftmaxWarps) o[i] = make_uint4(0, 0, 0, 0);
       if (a.lse && tid < heads) a.lse[row + tid] = -INFINITY;
       bool cut;
@@ -520,53 +570,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h0 = warp * 16 + (lane >> 2), h1 = h0 + 8;  // this lane's heads
     const float c2 = a.scale * kLog2e;
     const uint32_t quarter = static_cast<uint32_t>(warp * 32) << 16;
-    const int n = max(cur.left, 0);
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    bool whole = cur.c == 0;  // the CTA began the job at its first chunk
-    bool first_segment = true;
-    bool fresh = true;        // nothing of the job is in O yet
+    bool first_segment = true;  // the CTA's first job
     // After a wait that gave up the warp goes through the rest of its chunks
     // without touching TMEM or global memory, for the others' barriers.
     bool ok = true;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-      bool in = true;
-      if (lane == 0) in = tc::mbar_wait(bar, parity, abort_flag);
-      in = __shfl_sync(0xFFFFFFFFu, in, 0);
-      __syncwarp();
-      ok = ok && in;
-    };
+#pragma unroll 1
     for (int i = 0; i < n; i++) {
-      const int stage = i & 1;
-      const uint32_t par = (i >> 1) & 1;
-      wait(&sm->x_full[stage], par);  // orders the loaders' row mask before its reads here
-      const uint64_t valid = ok ? sm->valid[stage] : 0ull;
-      wait(&sm->s_full[stage], par);
-      uint32_t r[32];
+      const int stage = i & 1, slot = i % kRing;
+      ok = warp_wait(&sm->ring_full[slot], (i / kRing) & 1) && ok;
+      const uint32_t v0 = sm->ring[slot].valid[0], v1 = sm->ring[slot].valid[1];
+      const int32_t job = sm->ring[slot].job;
+      const uint32_t flags = ok ? sm->ring[slot].flags : 0u;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm->ring_free[slot]);
+      ok = warp_wait(&sm->s_full, i & 1) && ok;
+      float s0[16], s1[16];
       if (ok) {
         tc::tc_fence_after();
-        tmem_ld_s(tmem + quarter + kSCol + 64 * stage, r);
-        tc::tmem_ld_wait();
-        tc::tmem_ld32_pin(r);
-        tc::tc_fence_before();
-      } else {
+        uint32_t x[32], y[32];
 #pragma unroll
-        for (int k = 0; k < 32; k++) r[k] = 0u;
+        for (int part = 0; part < kParts; part += 2) {
+          tmem_ld_s(tmem + quarter + 64 * part, x);
+          tmem_ld_s(tmem + quarter + 64 * (part + 1), y);
+          tc::tmem_ld_wait();
+          tc::tmem_ld32_pin(x);
+          tc::tmem_ld32_pin(y);
+#pragma unroll
+          for (int u = 0; u < 16; u++) {
+            const int k = 4 * (u >> 1) + (u & 1);
+            const float p = __uint_as_float(x[k]) + __uint_as_float(y[k]);
+            const float q = __uint_as_float(x[k + 2]) + __uint_as_float(y[k + 2]);
+            s0[u] = part ? s0[u] + p : p;
+            s1[u] = part ? s1[u] + q : q;
+          }
+        }
+        tc::tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm->s_free[stage]);
-      float s0[16], s1[16];
+      if (lane == 0) tc::mbar_arrive(&sm->s_free);
       float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-      for (int u = 0; u < 8; u++) {
-        const uint32_t two = static_cast<uint32_t>(valid >> (8 * u + 2 * (lane & 3)));
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-          const bool in = (two >> k) & 1u;
-          s0[2 * u + k] = in ? __uint_as_float(r[4 * u + k]) * c2 : -INFINITY;
-          s1[2 * u + k] = in ? __uint_as_float(r[4 * u + 2 + k]) * c2 : -INFINITY;
-          t0 = fmaxf(t0, s0[2 * u + k]);
-          t1 = fmaxf(t1, s1[2 * u + k]);
-        }
+      for (int u = 0; u < 16; u++) {  // row 8 (u / 2) + 2 (lane % 4) + u % 2
+        const uint32_t bits = (u < 8 ? v0 : v1) >> (2 * (lane & 3));
+        const bool in = (bits >> (8 * ((u >> 1) & 3) + (u & 1))) & 1u;
+        s0[u] = in ? s0[u] * c2 : -INFINITY;
+        s1[u] = in ? s1[u] * c2 : -INFINITY;
+        t0 = fmaxf(t0, s0[u]);
+        t1 = fmaxf(t1, s1[u]);
       }
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) {
@@ -587,21 +638,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm->alpha[stage][h0] = a0;
         sm->alpha[stage][h1] = a1;
       }
-      uint32_t p0[8], p1[8];
-#pragma unroll
-      for (int u = 0; u < 8; u++) {
-        const float x0 = exp2_approx(s0[2 * u] - b0), x1 = exp2_approx(s0[2 * u + 1] - b0);
-        const float y0 = exp2_approx(s1[2 * u] - b1), y1 = exp2_approx(s1[2 * u + 1] - b1);
-        l0 += x0 + x1;
-        l1 += y0 + y1;
-        const __nv_bfloat162 px = __floats2bfloat162_rn(x0, x1), py = __floats2bfloat162_rn(y0, y1);
-        p0[u] = *reinterpret_cast<const uint32_t *>(&px);
-        p1[u] = *reinterpret_cast<const uint32_t *>(&py);
-      }
-      const uint32_t moved = bar_or(1, 32 * kSoftmaxWarps, !fresh && (a0 != 1.f || a1 != 1.f));
-      if (moved) wait(&sm->x_free[stage ^ 1], ((i - 1) >> 1) & 1);
+      const uint32_t moved = bar_or(1, 32 * kSoftmaxWarps, a0 != 1.f || a1 != 1.f);
+      if (moved) ok = warp_wait(&sm->x_free[stage ^ 1], ((i - 1) >> 1) & 1) && ok;
       if (moved && ok) {  // rescale O^T: lane = dim, columns = heads; the last second product is done
         tc::tc_fence_after();
+#pragma unroll 1
         for (int q = 0; q < 8; q++) {
           const uint32_t ta = tmem + quarter + kOCol + 32 * q;
           uint32_t v[32];
@@ -616,25 +657,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
       }
       // P^T line `head`: 16-byte pieces of eight rows, swizzled with head & 7 (free once chunk i - 2 is done)
-      if (i >= 2) wait(&sm->x_free[stage], ((i >> 1) - 1) & 1);
-      uint8_t *p = sP + stage * kPBytes;
+      if (i >= 2) ok = warp_wait(&sm->x_free[stage], ((i >> 1) - 1) & 1) && ok;
+      uint8_t *p0 = sP + stage * kPBytes + h0 * 128 + 4 * (lane & 3), *p1 = p0 + 8 * 128;
 #pragma unroll
       for (int u = 0; u < 8; u++) {
-        *reinterpret_cast<uint32_t *>(p + h0 * 128 + ((u ^ (h0 & 7)) << 4) + 4 * (lane & 3)) = p0[u];
-        *reinterpret_cast<uint32_t *>(p + h1 * 128 + ((u ^ (h1 & 7)) << 4) + 4 * (lane & 3)) = p1[u];
+        const float x0 = exp2_approx(s0[2 * u] - b0), x1 = exp2_approx(s0[2 * u + 1] - b0);
+        const float y0 = exp2_approx(s1[2 * u] - b1), y1 = exp2_approx(s1[2 * u + 1] - b1);
+        l0 += x0 + x1;
+        l1 += y0 + y1;
+        const __nv_bfloat162 px = __floats2bfloat162_rn(x0, x1), py = __floats2bfloat162_rn(y0, y1);
+        *reinterpret_cast<uint32_t *>(p0 + ((u ^ (h0 & 7)) << 4)) = *reinterpret_cast<const uint32_t *>(&px);
+        *reinterpret_cast<uint32_t *>(p1 + ((u ^ (h0 & 7)) << 4)) = *reinterpret_cast<const uint32_t *>(&py);
       }
       tc::fence_proxy_async_smem();
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm->p_full[stage]);
-      fresh = false;
 
-      const bool job_ends = cur.c + 1 == cur.n;
-      if (job_ends || i + 1 == n) {
-        // ---- this CTA's part of the job is done
-        const int32_t bt = cur.job / groups, g = cur.job % groups;
-        const bool out_now = whole && job_ends;
-        wait(&sm->x_free[stage], par);
+      if (flags & kLast) {  // this CTA's part of the job is done
+        const int32_t bt = job / groups, g = job % groups;
+        const bool out_now = flags & kWhole;
+        ok = warp_wait(&sm->x_free[stage], (i >> 1) & 1) && ok;
         tc::tc_fence_after();
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
@@ -643,21 +686,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int heads = min(kH, a.H - g * kH);
         const int64_t out_row = static_cast<int64_t>(bt) * a.H + g * kH;
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (first_segment ? 0 : 1);
-        if ((lane & 3) == 0 && ok) {
-#pragma unroll
-          for (int k = 0; k < 2; k++) {
-            const int h = k ? h1 : h0;
-            const float m = k ? m1 : m0, l = k ? l1 : l0;
-            if (out_now) {
-              sm->l[h] = l == 0.f ? 0.f : 1.f / l;
-              if (a.lse && h < heads) a.lse[out_row + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-            } else {
-              ws.ml[slot * kH + h] = make_float2(m, l);
-            }
+        const int64_t slot_o = 2 * static_cast<int64_t>(blockIdx.x) + (first_segment ? 0 : 1);
+        if ((lane & 3) < 2 && ok) {
+          const int h = (lane & 1) ? h1 : h0;
+          const float m = (lane & 1) ? m1 : m0, l = (lane & 1) ? l1 : l0;
+          if (out_now) {
+            sm->l[h] = l == 0.f ? 0.f : 1.f / l;
+            if (a.lse && h < heads) a.lse[out_row + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+          } else {
+            ws.ml[slot_o * kH + h] = make_float2(m, l);
           }
         }
         bar_or(1, 32 * kSoftmaxWarps, 0u);  // sm->l is in
+#pragma unroll 1
         for (int q = 0; q < 8 && ok; q++) {
           const int d = 128 * (q >> 1) + 32 * warp + lane, hb = 32 * (q & 1);
           uint32_t v[32];
@@ -665,16 +706,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tmem_ld_wait();
           tc::tmem_ld32_pin(v);
           if (out_now) {
-            uint16_t *o = static_cast<uint16_t *>(a.out) + out_row * kD + d;
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + (out_row + hb) * kD + d;
 #pragma unroll
             for (int h = 0; h < 32; h++)
-              if (hb + h < heads)
-                o[(hb + h) * kD] = static_cast<uint16_t>(bf16_bits(__uint_as_float(v[h]) * sm->l[hb + h]));
+              if (hb + h < heads) o[h * kD] = __float2bfloat16_rn(__uint_as_float(v[h]) * sm->l[hb + h]);
           } else {
-            float *o = ws.o + slot * kH * kD + d;
+            float *o = ws.o + (slot_o * kH + hb) * kD + d;
 #pragma unroll
             for (int h = 0; h < 32; h++)
-              if (hb + h < heads) o[(hb + h) * kD] = __uint_as_float(v[h]);
+              if (hb + h < heads) o[h * kD] = __uint_as_float(v[h]);
           }
         }
         tc::tc_fence_before();
@@ -682,11 +722,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) tc::mbar_arrive(&sm->o_free);
         m0 = m1 = -INFINITY;
         l0 = l1 = 0.f;
-        whole = true;
         first_segment = false;
-        fresh = true;
       }
-      cur.next(a, groups, shift);
     }
   }
   tc::tc_fence_before();
@@ -698,85 +735,129 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && sm->abort) raise_status(ws.status, LIDX_DEV_TIMEOUT);
 }
 
-// Joins the partial results of jobs that span CTAs.  An item is such a job, a
-// head and a quarter of its dims: eight warps take every eighth partial, lane
-// l dims [4l, 4l + 4) of the quarter.
+// Joins the partial results of jobs that span CTAs.  A job with few partials
+// is 64 items (a head each), one with many 256 (a head and a quarter of its
+// dims): in a CTA of 128 threads, 128 or 32 take four dims each, and one or
+// four groups of them every partial or every fourth.
 __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const lidx_paged_attn_args a, const Jobs jobs,
                                                                          const Scratch ws) {
-  __shared__ float4 acc_s[kMergeThreads / 32][32];
-  __shared__ float2 ml_s[kMergeThreads / 32];
-  __shared__ int32_t list[kMaxCtas], count[kMergeThreads / 32];
+  __shared__ Split list[kMaxCtas];
+  __shared__ int32_t base[kMaxCtas + 1];  // first item of each
+  __shared__ int32_t sums[2][kMergeThreads / 32];
+  __shared__ float4 acc_s[kMergeThreads];
+  __shared__ float2 ml_s[kMergeThreads];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   pdl_wait();  // the partial results come from the previous kernel
-  // the split jobs, in the same order in every CTA (kMaxCtas <= kMergeThreads)
-  const bool mine = tid < jobs.G && ws.split[tid].job >= 0;
-  const uint32_t flags = __ballot_sync(0xFFFFFFFFu, mine);
-  if (lane == 0) count[warp] = __popc(flags);
-  __syncthreads();
-  int n_list = 0, at = __popc(flags & ((1u << lane) - 1u));
-#pragma unroll
-  for (int w = 0; w < kMergeThreads / 32; w++) {
-    if (w < warp) at += count[w];
-    n_list += count[w];
-  }
-  if (mine) list[at] = tid;
-  __syncthreads();
-  constexpr int kPerJob = kH * 4;
-  const int items = n_list * kPerJob;
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int32_t g = list[item / kPerJob], h = (item % kPerJob) >> 2, quarter = item & 3;
-    const Split sp = ws.split[g];
-    const int32_t start = sp.start, end = sp.end, total = sp.total;
-    const int32_t bt = sp.job / jobs.groups, group = sp.job % jobs.groups;
-    if (h >= min(kH, a.H - group * kH)) continue;
-    const int32_t from = owner(start, jobs.G, total), last = owner(end - 1, jobs.G, total);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float m = -INFINITY, l = 0.f;
-    for (int32_t c = from + warp; c <= last; c += kMergeThreads / 32) {
-      const int32_t s = range_start(c, jobs.G, total);
-      if (s == range_start(c + 1, jobs.G, total)) continue;  // an empty range
-      // the job is the CTA's first one unless the CTA began with an earlier job
-      const int64_t slot = 2 * static_cast<int64_t>(c) + (s < start ? 1 : 0);
-      const float2 w = ws.ml[slot * kH + h];
-      if (w.x == -INFINITY && w.y == 0.f) continue;  // no row of it counts (a NaN sum does)
-      const float4 v = reinterpret_cast<const float4 *>(ws.o + (slot * kH + h) * kD + 128 * quarter)[lane];
-      const float mn = fmaxf(m, w.x), f = m == mn ? 1.f : exp2f(m - mn), e = w.x == mn ? 1.f : exp2f(w.x - mn);
-      l = fmaf(l, f, e * w.y);
-      acc.x = fmaf(acc.x, f, e * v.x);
-      acc.y = fmaf(acc.y, f, e * v.y);
-      acc.z = fmaf(acc.z, f, e * v.z);
-      acc.w = fmaf(acc.w, f, e * v.w);
-      m = mn;
+  // the split jobs, in the same order in every CTA
+  int n_list = 0, n_items = 0;
+  for (int g0 = 0; g0 < jobs.G; g0 += kMergeThreads) {
+    Split sp;
+    sp.job = -1;
+    if (g0 + tid < jobs.G) sp = ws.split[g0 + tid];
+    int items = 0;
+    if (sp.job >= 0)
+      items = owner(sp.end - 1, jobs.G, sp.total) - owner(sp.start, jobs.G, sp.total) >= kFewPartials ? 4 * kH : kH;
+    const int incl = warp_inclusive_scan(items), flag = sp.job >= 0 ? 1 : 0;
+    const int rank = warp_inclusive_scan(flag);
+    if (lane == 31) {
+      sums[0][warp] = incl;
+      sums[1][warp] = rank;
     }
     __syncthreads();
-    acc_s[warp][lane] = acc;
-    if (lane == 0) ml_s[warp] = make_float2(m, l);
-    __syncthreads();
-    if (warp != 0) continue;
-    m = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kMergeThreads / 32; w++) m = fmaxf(m, ml_s[w].x);
-    l = 0.f;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    int at_item = n_items + incl - items, at = n_list + rank - flag;
 #pragma unroll
     for (int w = 0; w < kMergeThreads / 32; w++) {
-      const float2 x = ml_s[w];
-      if (x.x == -INFINITY && x.y == 0.f) continue;
-      const float e = x.x == m ? 1.f : exp2f(x.x - m);
-      const float4 v = acc_s[w][lane];
-      l = fmaf(e, x.y, l);
-      acc.x = fmaf(e, v.x, acc.x);
-      acc.y = fmaf(e, v.y, acc.y);
-      acc.z = fmaf(e, v.z, acc.z);
-      acc.w = fmaf(e, v.w, acc.w);
+      if (w < warp) {
+        at_item += sums[0][w];
+        at += sums[1][w];
+      }
+      n_items += sums[0][w];
+      n_list += sums[1][w];
+    }
+    if (flag) {
+      list[at] = sp;
+      base[at] = at_item;
+    }
+    __syncthreads();
+  }
+  if (tid == 0) base[n_list] = n_items;
+  __syncthreads();
+#pragma unroll 1
+  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
+    int lo = 0, hi = n_list - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (base[mid] <= item) lo = mid;
+      else hi = mid - 1;
+    }
+    const Split sp = list[lo];
+    const bool many = base[lo + 1] - base[lo] > kH;
+    const int h = many ? (item - base[lo]) >> 2 : item - base[lo];
+    const int32_t bt = sp.job / jobs.groups, group = sp.job % jobs.groups;
+    if (h >= min(kH, a.H - group * kH)) continue;
+    const int32_t from = owner(sp.start, jobs.G, sp.total), last = owner(sp.end - 1, jobs.G, sp.total);
+    const int d4 = many ? 32 * ((item - base[lo]) & 3) + lane : tid;  // this thread's four dims
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = -INFINITY, l = 0.f;
+    const int step = many ? 4 : 1;
+#pragma unroll 1
+    for (int32_t c0 = from + (many ? warp : 0); c0 <= last; c0 += kBatch * step) {
+      float4 v[kBatch];
+      float2 w[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; k++) {
+        const int32_t c = c0 + k * step;
+        w[k] = make_float2(-INFINITY, 0.f);
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c <= last) {
+          const int32_t s = range_start(c, jobs.G, sp.total);
+          if (s != range_start(c + 1, jobs.G, sp.total)) {  // not an empty range
+            // the job is the CTA's first one unless the CTA began with an earlier job
+            const int64_t slot = 2 * static_cast<int64_t>(c) + (s < sp.start ? 1 : 0);
+            w[k] = ws.ml[slot * kH + h];
+            v[k] = reinterpret_cast<const float4 *>(ws.o + (slot * kH + h) * kD)[d4];
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; k++) {
+        if (w[k].x == -INFINITY && w[k].y == 0.f) continue;  // no row of it counts (a NaN sum does)
+        const float mn = fmaxf(m, w[k].x), f = m == mn ? 1.f : exp2f(m - mn), e = w[k].x == mn ? 1.f : exp2f(w[k].x - mn);
+        l = fmaf(l, f, e * w[k].y);
+        acc.x = fmaf(acc.x, f, e * v[k].x);
+        acc.y = fmaf(acc.y, f, e * v[k].y);
+        acc.z = fmaf(acc.z, f, e * v[k].z);
+        acc.w = fmaf(acc.w, f, e * v[k].w);
+        m = mn;
+      }
+    }
+    if (many) {  // the four warps' parts, joined by the first
+      __syncthreads();
+      acc_s[tid] = acc;
+      ml_s[tid] = make_float2(m, l);
+      __syncthreads();
+      if (warp != 0) continue;
+#pragma unroll
+      for (int w = 1; w < 4; w++) {
+        const float2 x = ml_s[32 * w + lane];
+        if (x.x == -INFINITY && x.y == 0.f) continue;
+        const float mn = fmaxf(m, x.x), f = m == mn ? 1.f : exp2f(m - mn), e = x.x == mn ? 1.f : exp2f(x.x - mn);
+        const float4 v = acc_s[32 * w + lane];
+        l = fmaf(l, f, e * x.y);
+        acc.x = fmaf(acc.x, f, e * v.x);
+        acc.y = fmaf(acc.y, f, e * v.y);
+        acc.z = fmaf(acc.z, f, e * v.z);
+        acc.w = fmaf(acc.w, f, e * v.w);
+        m = mn;
+      }
     }
     const float il = l == 0.f ? 0.f : 1.f / l;
     const int64_t row = static_cast<int64_t>(bt) * a.H + group * kH + h;
-    const uint2 o = make_uint2(bf16_bits(acc.x * il) | (bf16_bits(acc.y * il) << 16),
-                               bf16_bits(acc.z * il) | (bf16_bits(acc.w * il) << 16));
-    reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * kD + 128 * quarter)[lane] = o;
-    if (a.lse && quarter == 0 && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * il, acc.y * il), y = __floats2bfloat162_rn(acc.z * il, acc.w * il);
+    reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * kD)[d4] =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+    if (a.lse && d4 == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 
@@ -853,7 +934,7 @@ cudaError_t launch_paged_attn(const lidx_paged_attn_args &a, void *ws, cudaStrea
     default: e = launch<LIDX_BF16>(tm, a, j, s, st); break;
   }
   if (e != cudaSuccess) return e;
-  return launch_kernel(paged_attn_merge_kernel, dim3(4 * sm_count()), dim3(kMergeThreads), 0, st, true, a, j, s);
+  return launch_kernel(paged_attn_merge_kernel, dim3(8 * sm_count()), dim3(kMergeThreads), 0, st, true, a, j, s);
 }
 
 }  // namespace lidx
