@@ -54,6 +54,36 @@ __device__ __forceinline__ void e2m1x8_to_bf16x2(uint32_t w, uint32_t (&o)[4]) {
   o[3] = __byte_perm(lo1, hi1, 0x7362);
 }
 
+// Eight E2M1 codes times their block's scale 2^(c - 127) as four bf16 pairs,
+// exactly, with half of the work on the multiply pipe (the byte permutes above
+// all run on the integer pipe, which bounds the attention's loader).  The
+// three magnitude bits of a code, put at bits 8..6 of a bf16, are its value
+// times 2^-126 (0.5 is a bf16 subnormal there), so one product with
+// 2^(126 + e) decodes and scales.  B * (2^6 + 2^18) puts a byte's two codes in
+// place in the two halves; scales above 2 take a second product.
+struct E2m1Scale {
+  uint32_t s1, s2;
+  bool two;  // the same in all lanes of a converged warp
+  __device__ __forceinline__ explicit E2m1Scale(uint32_t c) {
+    s1 = c == 0xFFu ? 0x7FC0u : (min(c, 128u) + 126u) << 7;
+    s2 = c > 128u ? (c - 1u) << 7 : 0x3F80u;
+    s1 |= s1 << 16;
+    s2 |= s2 << 16;
+    two = __any_sync(0xFFFFFFFFu, c > 128u);
+  }
+  __device__ __forceinline__ void expand(uint32_t w, uint32_t (&o)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const uint32_t x = ((w >> (8 * i)) & 0xFFu) * 0x00040040u;
+      o[i] = mul_bf16x2(((x * 64u) & 0x80008000u) | (x & 0x01C001C0u), s1);
+    }
+    if (two) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) o[i] = mul_bf16x2(o[i], s2);
+    }
+  }
+};
+
 __device__ __forceinline__ float bf16x2_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16x2_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 

@@ -25,9 +25,12 @@
 //   * four softmax warps read S in the 16x256b shape, in which the 32 lanes of
 //     a warp share the 16 heads of its TMEM quarter (8 head pairs x 4 column
 //     groups), so row maxima take two shuffles and no lane idles.  S is free
-//     for the next chunk as soon as it is read.  The running maximum moves
-//     only when it rises by more than 8 (base 2); then the O so far is
-//     rescaled in TMEM.  Sums are of the fp32 probabilities.
+//     for the next chunk as soon as it is read.  The running maximum is only a
+//     reference (p = 2^(s - m) may exceed 1), so it moves only when it rises
+//     by more than 32 (base 2), and only then is the O so far rescaled in
+//     TMEM: at 8 one of the 64 heads made most chunks pay for it.  Sums are of
+//     the fp32 probabilities; floating point loses nothing by a common factor
+//     up to 2^32.
 //   P is rounded to bf16 for the second product: 2^-9 of each probability,
 //   independent errors that average out to less than the bf16 output's own
 //   rounding.
@@ -61,11 +64,12 @@ constexpr int kParts = 4;                // partial sums of S, at columns 64 i
 constexpr uint32_t kOCol = 64 * kParts;  // O^T tile t at columns kOCol + 64 t
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 8.f;             // base-2 headroom of the reference maximum
+constexpr float kLazy = 32.f;            // base-2 headroom of the reference maximum
 constexpr int kMergeThreads = 128;
 constexpr int kFewPartials = 8;          // up to as many are joined by one thread a dim
 constexpr int kBatch = 8;                // partials whose loads are in flight together
 constexpr int kMaxCtas = 256;            // one CTA per SM
+constexpr uint32_t kIdleLimit = 1u << 24;  // rounds without work after which the issuing warp gives up (seconds)
 
 // What the scout says about a chunk.
 constexpr uint32_t kFirst = 1u;  // the first chunk of its job in this CTA
@@ -115,28 +119,60 @@ struct Scratch {
 // The job list.
 struct Jobs {
   int32_t n;       // B * T * groups of heads
-  int32_t groups;  // of 64 heads
+  int32_t group_shift;  // 0: one group of up to 64 heads, 1: two
   int32_t G;       // CTAs
 };
 
-__device__ __forceinline__ int32_t range_start(int32_t g, int32_t G, int32_t total) {
-  return static_cast<int32_t>(static_cast<int64_t>(g) * total / G);
-}
-
-// the CTA that holds chunk c
-__device__ __forceinline__ int32_t owner(int32_t c, int32_t G, int32_t total) {
-  return static_cast<int32_t>(((static_cast<int64_t>(c) + 1) * G - 1) / total);
-}
+// The chunks are dealt out in runs of base or base + 1 (the first `more` CTAs).
+struct Deal {
+  int32_t base, more;
+  __device__ __forceinline__ Deal(int32_t total, int32_t G) : base(total / G), more(total % G) {}
+  __device__ __forceinline__ int32_t start(int32_t g) const { return g * base + min(g, more); }  // CTA g's first chunk
+  __device__ __forceinline__ int32_t owner(int32_t c) const {  // the CTA that holds chunk c
+    const int32_t big = more * (base + 1);
+    return c < big ? c / (base + 1) : more + (c - big) / max(base, 1);
+  }
+};
 
 // Entries of job's row list: rows for the dense case, rows of the listed blocks otherwise.
-__device__ __forceinline__ int32_t job_rows(const lidx_paged_attn_args &a, int32_t job, int groups, int shift) {
-  const int32_t bt = job / groups;
+__device__ __forceinline__ int32_t job_rows(const lidx_paged_attn_args &a, int32_t job, int gs, int shift) {
+  const int32_t bt = job >> gs;
   if (a.blocks) return (a.n_sel ? min(max(__ldg(a.n_sel + bt), 0), a.n_blocks) : a.n_blocks) << shift;
   bool cut;
   return max(cut_len(__ldg(a.len + bt / a.T), a.cache, cut) - (a.T - 1 - bt % a.T), 0);
 }
-__device__ __forceinline__ int32_t job_chunks(const lidx_paged_attn_args &a, int32_t job, int groups, int shift) {
-  return (job_rows(a, job, groups, shift) + kRows - 1) / kRows;
+__device__ __forceinline__ int32_t job_chunks(const lidx_paged_attn_args &a, int32_t job, int gs, int shift) {
+  return (job_rows(a, job, gs, shift) + kRows - 1) / kRows;
+}
+
+__device__ __forceinline__ bool elect() {  // true in one lane of a converged warp, always the same
+  uint32_t r;
+  asm volatile(
+      "{\n"
+      " .reg .pred p;\n"
+      " elect.sync _|p, 0xFFFFFFFF;\n"
+      " selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(r));
+  return r != 0u;
+}
+
+// Whether the phase with `parity` has completed, without waiting.
+__device__ __forceinline__ bool test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n"
+      " .reg .pred p;\n"
+      " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(ok)
+      : "r"(tc::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
+__device__ __forceinline__ bool ready(uint64_t *bar, uint32_t parity) {  // the same answer in all lanes
+  return __all_sync(0xFFFFFFFFu, test(bar, parity));
 }
 
 // tc::mbar_wait with its loop kept rolled.
@@ -254,13 +290,12 @@ struct Slab {
       if (kFmt == LIDX_BF16) {
         *reinterpret_cast<uint4 *>(row + ((piece ^ (r & 7)) << 4)) = v[it];
       } else if (kFmt == LIDX_E2M1) {
-        const uint32_t s = e8m0_to_bf16x2(scale[it]);
+        const E2m1Scale s(scale[it]);
 #pragma unroll
         for (int i = 0; i < 4; i++) {
           uint32_t o[4];
-          e2m1x8_to_bf16x2(w[i], o);
-          *reinterpret_cast<uint4 *>(row + (((4 * piece + i) ^ (r & 7)) << 4)) =
-              make_uint4(mul_bf16x2(o[0], s), mul_bf16x2(o[1], s), mul_bf16x2(o[2], s), mul_bf16x2(o[3], s));
+          s.expand(w[i], o);
+          *reinterpret_cast<uint4 *>(row + (((4 * piece + i) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
       } else {
         const uint32_t s = e8m0_to_bf16x2(scale[it]);
@@ -305,8 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *sP = sX + 2 * kXBytes;  // stage i at sP + i * kPBytes
   Smem *sm = reinterpret_cast<Smem *>(sP + 2 * kPBytes);
   volatile uint32_t *abort_flag = &sm->abort;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int groups = jobs.groups;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // the same in all lanes, for the compiler to see
+  const int gs = jobs.group_shift;
 
   if (tid == 0) {
     tc::mbar_init(&sm->q_full, 1);
@@ -344,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int j0 = min(tid * per, jobs.n), j1 = min(j0 + per, jobs.n);
     int32_t mine = 0;
 #pragma unroll 1
-    for (int j = j0; j < j1; j++) mine += job_chunks(a, j, groups, shift);
+    for (int j = j0; j < j1; j++) mine += job_chunks(a, j, gs, shift);
     const int32_t incl = warp_inclusive_scan(mine);
     if (lane == 31) sm->scan[warp] = incl;
     __syncthreads();
@@ -356,13 +392,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w < warp) before += s;
       total += s;
     }
-    my0 = range_start(blockIdx.x, jobs.G, total);
-    my1 = range_start(blockIdx.x + 1, jobs.G, total);
+    const Deal deal(total, jobs.G);
+    my0 = deal.start(blockIdx.x);
+    my1 = deal.start(blockIdx.x + 1);
     if (before <= my0 && my0 < before + mine) {
       int32_t at = before;
 #pragma unroll 1
       for (int j = j0; j < j1; j++) {
-        const int32_t m = job_chunks(a, j, groups, shift);
+        const int32_t m = job_chunks(a, j, gs, shift);
         if (at <= my0 && my0 < at + m) {
           sm->job = j;
           sm->chunk = my0 - at;
@@ -395,9 +432,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       sp.start = my0 - c;
       sp.end = 0;
       sp.total = total;
-      if (c > 0 && range_start(owner(my0 - 1, jobs.G, total), jobs.G, total) <= sp.start) {
+      const Deal deal(total, jobs.G);
+      if (c > 0 && deal.start(static_cast<int32_t>(blockIdx.x) - 1) <= sp.start) {
         sp.job = job;
-        sp.end = sp.start + (job_rows(a, job, groups, shift) + kRows - 1) / kRows;
+        sp.end = sp.start + (job_rows(a, job, gs, shift) + kRows - 1) / kRows;
       }
       ws.split[blockIdx.x] = sp;
     }
@@ -408,9 +446,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           job++;
           c = 0;
         }
-        while ((rows = job_rows(a, job, groups, shift)) == 0) job++;
+        while ((rows = job_rows(a, job, gs, shift)) == 0) job++;
         left = (rows + kRows - 1) / kRows - c;
-        const int32_t bt = job / groups;
+        const int32_t bt = job >> gs;
         bool cut;
         seen = cut_len(__ldg(a.len + bt / a.T), a.cache, cut) - (a.T - 1 - bt % a.T);
         bounds |= cut;
@@ -418,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         flags = kFirst;
       }
       if (left == 1 || i + 1 == n) flags |= kLast | (whole && left == 1 ? kWhole : 0u);
-      const int32_t bt = job / groups;
+      const int32_t bt = job >> gs;
       const int32_t p0 = entry_row(a, bt, shift, c * kRows + lane, seen, rows, bounds);
       const int32_t p1 = entry_row(a, bt, shift, c * kRows + 32 + lane, seen, rows, bounds);
       const uint32_t v0 = __ballot_sync(0xFFFFFFFFu, p0 >= 0), v1 = __ballot_sync(0xFFFFFFFFu, p1 >= 0);
@@ -470,52 +508,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMma) {
     // ------------------------------------------------- the matrix products
-    if (lane == 0) {
-      const uint32_t idesc_s = tc::idesc_bf16(64, 64), idesc_o = tc::idesc_bf16(128, 64, true, false);
-      const uint64_t q_desc = tc::desc_kmajor_sw128(tc::smem_u32(sQ));
-      const uint64_t x_desc = tc::desc_kmajor_sw128(tc::smem_u32(sX));
-      const uint64_t xt_desc = tc::desc_mnmajor_sw128(tc::smem_u32(sX), kPanel, 1024);
-      const uint64_t p_desc = tc::desc_kmajor_sw128(tc::smem_u32(sP));
-      int begun = 0, q_loads = 0;  // jobs begun, up to chunk i
-      uint32_t flags = 0u;
-      bool ok = true;
+    // The whole warp goes through the loop, so that descriptors and flags stay
+    // in uniform registers, and one elected lane issues: with a single lane in
+    // the loop each product took 100 cycles to issue, whatever its shape.
+    const uint32_t idesc_s = tc::idesc_bf16(64, 64), idesc_o = tc::idesc_bf16(128, 64, true, false);
+    const uint64_t q_desc = tc::desc_kmajor_sw128(tc::smem_u32(sQ));
+    const uint64_t x_desc = tc::desc_kmajor_sw128(tc::smem_u32(sX));
+    const uint64_t xt_desc = tc::desc_mnmajor_sw128(tc::smem_u32(sX), kPanel, 1024);
+    const uint64_t p_desc = tc::desc_kmajor_sw128(tc::smem_u32(sP));
+    int si = 0, oi = 0;                  // the next chunk of S and of O
+    int s_jobs = 0, o_jobs = 0;          // jobs begun by then
+    uint32_t firsts = 0u;                // bit i % 2: chunk i is the first of its job
+    int state = 0;                       // of chunk si: 0 unknown, 1 known and Q wanted, 2 Q on its way, 3 Q there
+    uint32_t idle = 0;
 #pragma unroll 1
-      for (int i = 0; i <= n && ok; i++) {  // S of chunk i, O of chunk i - 1
-        const bool prev_first = flags & kFirst;
-        const int prev_begun = begun;
-        if (i < n) {
-          const int slot = i % kRing;
-          ok = wait_for(&sm->ring_full[slot], (i / kRing) & 1, abort_flag);
-          if (!ok) break;
-          flags = sm->ring[slot].flags;
-          const int32_t job = sm->ring[slot].job;
-          tc::mbar_arrive(&sm->ring_free[slot]);
-          if (flags & kFirst) {
-            begun++;
-            if (i > 0) ok = wait_for(&sm->s_full, (i - 1) & 1, abort_flag);  // Q has been read for the last time
-            if (!ok) break;
-            tc::mbar_arrive_expect_tx(&sm->q_full, kQBytes);
-            q_loads++;
-#pragma unroll 1
-            for (int p = 0; p < 8; p++)
-              tma_load_3d(sQ + p * kPanel, &tm_q, &sm->q_full, 64 * p, (job % groups) * kH, job / groups);
+    while (oi < n) {
+      bool moved = false;
+      if (si < n && si < oi + 2) {
+        if (state == 0 && ready(&sm->ring_full[si % kRing], (si / kRing) & 1)) {
+          const Chunk &k = sm->ring[si % kRing];
+          state = (k.flags & kFirst) ? 1 : 3;
+          firsts = (firsts & ~(1u << (si & 1))) | ((k.flags & kFirst) << (si & 1));
+          if (state == 3) {
+            __syncwarp();
+            if (elect()) tc::mbar_arrive(&sm->ring_free[si % kRing]);
           }
         }
-        // S first, so that it runs while the softmax of chunk i - 1 does; where it waits for a new Q, O first
-        const int s_at = (i < n && (flags & kFirst)) ? 1 : 0;
+        if (state == 1 && (si == 0 || ready(&sm->s_full, (si - 1) & 1))) {  // Q has been read for the last time
+          const int32_t job = sm->ring[si % kRing].job;
+          __syncwarp();
+          if (elect()) {
+            tc::mbar_arrive(&sm->ring_free[si % kRing]);
+            tc::mbar_arrive_expect_tx(&sm->q_full, kQBytes);
 #pragma unroll 1
-        for (int half = 0; half < 2 && ok; half++) {
-          if (half == s_at) {
-            if (i == n) continue;
-            const int stage = i & 1;
-            if (flags & kFirst) ok = wait_for(&sm->q_full, (begun - 1) & 1, abort_flag);
-            ok = ok && wait_for(&sm->x_full[stage], (i >> 1) & 1, abort_flag);
-            if (i > 0) ok = ok && wait_for(&sm->s_free, (i - 1) & 1, abort_flag);
-            if (!ok) break;
-            tc::tc_fence_after();
-            // step k: panel k / 4, 32 bytes (k % 4) into it; part p sums panels 2p and 2p + 1
-            const uint64_t xd = x_desc + stage * (kXBytes >> 4);
-#pragma unroll 1
+            for (int p = 0; p < 8; p++)
+              tma_load_3d(sQ + p * kPanel, &tm_q, &sm->q_full, 64 * p, (job & ((1 << gs) - 1)) * kH, job >> gs);
+          }
+          __syncwarp();
+          s_jobs++;
+          state = 2;
+        }
+        if (state == 2 && ready(&sm->q_full, (s_jobs - 1) & 1)) state = 3;
+        if (state == 3 && ready(&sm->x_full[si & 1], (si >> 1) & 1) && (si == 0 || ready(&sm->s_free, (si - 1) & 1))) {
+          tc::tc_fence_after();
+          // step k: panel k / 4, 32 bytes (k % 4) into it; part p sums panels 2p and 2p + 1
+          const uint64_t xd = x_desc + (si & 1) * (kXBytes >> 4);
+          if (elect()) {
+#pragma unroll
             for (int j = 0; j < 8; j++) {
 #pragma unroll
               for (int part = 0; part < kParts; part++) {
@@ -524,40 +563,52 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             tc::mma_commit(&sm->s_full);
-          } else {
-            if (i == 0) continue;
-            const int stage = (i - 1) & 1;
-            if (prev_first && prev_begun > 1) ok = wait_for(&sm->o_free, prev_begun & 1, abort_flag);
-            ok = ok && wait_for(&sm->p_full[stage], ((i - 1) >> 1) & 1, abort_flag);
-            if (!ok) break;
-            tc::tc_fence_after();
-            const uint64_t xd = xt_desc + stage * (kXBytes >> 4), pd = p_desc + stage * (kPBytes >> 4);
-#pragma unroll 1
+          }
+          __syncwarp();
+          si++;
+          state = 0;
+          moved = true;
+        }
+      }
+      if (oi < si && ready(&sm->p_full[oi & 1], (oi >> 1) & 1)) {
+        const bool first = (firsts >> (oi & 1)) & 1u;
+        if (!first || o_jobs == 0 || ready(&sm->o_free, (o_jobs - 1) & 1)) {
+          tc::tc_fence_after();
+          const uint64_t xd = xt_desc + (oi & 1) * (kXBytes >> 4), pd = p_desc + (oi & 1) * (kPBytes >> 4);
+          if (elect()) {
+#pragma unroll
             for (int kk = 0; kk < kRows / 16; kk++) {
 #pragma unroll
               for (int dt = 0; dt < 4; dt++)
                 tc::mma_bf16(tmem + kOCol + 64 * dt, xd + ((2 * dt * kPanel + kk * 2048) >> 4), pd + kk * 2, idesc_o,
-                             !prev_first || kk > 0);
+                             !first || kk > 0);
             }
-            tc::mma_commit(&sm->x_free[stage]);
+            tc::mma_commit(&sm->x_free[oi & 1]);
           }
+          __syncwarp();
+          o_jobs += first;
+          oi++;
+          moved = true;
         }
       }
-      // a wait that gave up may leave copies and products in flight: they end before the CTA does
-      if (!ok) {
-        volatile uint32_t unused = 0;
-        if (q_loads > 0) wait_for(&sm->q_full, (q_loads - 1) & 1, &unused);
-        tc::mma_commit(&sm->drained);
-        wait_for(&sm->drained, 0, &unused);
-      }
+      idle = moved ? 0u : idle + 1u;
+      if (idle > kIdleLimit) *abort_flag = 1u;
+      if (__any_sync(0xFFFFFFFFu, *abort_flag != 0u)) break;
+    }
+    if (oi < n) {  // a wait gave up: the copies and products in flight end before the CTA does
+      volatile uint32_t unused = 0;
+      if (state >= 2 && s_jobs > 0) wait_for(&sm->q_full, (s_jobs - 1) & 1, &unused);
+      if (elect()) tc::mma_commit(&sm->drained);
+      __syncwarp();
+      wait_for(&sm->drained, 0, &unused);
     }
   } else {
     // ------------------------------------------------------------ softmax
     // first, while the first rows are on their way: the jobs without rows, dealt out to the CTAs
 #pragma unroll 1
     for (int32_t j = blockIdx.x; j < jobs.n; j += jobs.G) {
-      if (job_rows(a, j, groups, shift) > 0) continue;
-      const int32_t bt = j / groups, g = j % groups, heads = min(kH, a.H - g * kH);
+      if (job_rows(a, j, gs, shift) > 0) continue;
+      const int32_t bt = j >> gs, g = j & ((1 << gs) - 1), heads = min(kH, a.H - g * kH);
       const int64_t row = static_cast<int64_t>(bt) * a.H + g * kH;
       uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + row * kD);
 #pragma unroll 1
@@ -675,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) tc::mbar_arrive(&sm->p_full[stage]);
 
       if (flags & kLast) {  // this CTA's part of the job is done
-        const int32_t bt = job / groups, g = job % groups;
+        const int32_t bt = job >> gs, g = job & ((1 << gs) - 1);
         const bool out_now = flags & kWhole;
         ok = warp_wait(&sm->x_free[stage], (i >> 1) & 1) && ok;
         tc::tc_fence_after();
@@ -756,8 +807,10 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const l
     sp.job = -1;
     if (g0 + tid < jobs.G) sp = ws.split[g0 + tid];
     int items = 0;
-    if (sp.job >= 0)
-      items = owner(sp.end - 1, jobs.G, sp.total) - owner(sp.start, jobs.G, sp.total) >= kFewPartials ? 4 * kH : kH;
+    if (sp.job >= 0) {
+      const Deal deal(sp.total, jobs.G);
+      items = deal.owner(sp.end - 1) - deal.owner(sp.start) >= kFewPartials ? 4 * kH : kH;
+    }
     const int incl = warp_inclusive_scan(items), flag = sp.job >= 0 ? 1 : 0;
     const int rank = warp_inclusive_scan(flag);
     if (lane == 31) {
@@ -794,9 +847,10 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const l
     const Split sp = list[lo];
     const bool many = base[lo + 1] - base[lo] > kH;
     const int h = many ? (item - base[lo]) >> 2 : item - base[lo];
-    const int32_t bt = sp.job / jobs.groups, group = sp.job % jobs.groups;
+    const int32_t bt = sp.job >> jobs.group_shift, group = sp.job & ((1 << jobs.group_shift) - 1);
     if (h >= min(kH, a.H - group * kH)) continue;
-    const int32_t from = owner(sp.start, jobs.G, sp.total), last = owner(sp.end - 1, jobs.G, sp.total);
+    const Deal deal(sp.total, jobs.G);
+    const int32_t from = deal.owner(sp.start), last = deal.owner(sp.end - 1);
     const int d4 = many ? 32 * ((item - base[lo]) & 3) + lane : tid;  // this thread's four dims
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = -INFINITY, l = 0.f;
@@ -811,13 +865,10 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const l
         w[k] = make_float2(-INFINITY, 0.f);
         v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (c <= last) {
-          const int32_t s = range_start(c, jobs.G, sp.total);
-          if (s != range_start(c + 1, jobs.G, sp.total)) {  // not an empty range
-            // the job is the CTA's first one unless the CTA began with an earlier job
-            const int64_t slot = 2 * static_cast<int64_t>(c) + (s < sp.start ? 1 : 0);
-            w[k] = ws.ml[slot * kH + h];
-            v[k] = reinterpret_cast<const float4 *>(ws.o + (slot * kH + h) * kD)[d4];
-          }
+          // the job is the CTA's first one unless the CTA began with an earlier job
+          const int32_t slot = 2 * c + (deal.start(c) < sp.start ? 1 : 0);
+          w[k] = ws.ml[slot * kH + h];
+          v[k] = reinterpret_cast<const float4 *>(ws.o + static_cast<size_t>(slot * kH + h) * kD)[d4];
         }
       }
 #pragma unroll
@@ -880,7 +931,7 @@ int64_t job_count(const lidx_paged_attn_args &a) { return static_cast<int64_t>(a
 
 Jobs plan(const lidx_paged_attn_args &a) {
   Jobs j;
-  j.groups = (a.H + kH - 1) / kH;
+  j.group_shift = a.H > kH ? 1 : 0;
   j.n = static_cast<int32_t>(job_count(a));
   j.G = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(std::min(sm_count(), kMaxCtas), job_count(a) * most_chunks(a))));
   return j;
