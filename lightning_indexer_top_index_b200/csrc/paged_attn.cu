@@ -65,9 +65,8 @@ constexpr uint32_t kOCol = 64 * kParts;  // O^T tile t at columns kOCol + 64 t
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 32.f;            // base-2 headroom of the reference maximum
-constexpr int kMergeThreads = 128;
-constexpr int kFewPartials = 8;          // up to as many are joined by one thread a dim
-constexpr int kBatch = 8;                // partials whose loads are in flight together
+constexpr int kMergeThreads = 256;
+constexpr int kBatch = 4;                // partials of a warp whose loads are in flight together
 constexpr int kMaxCtas = 256;            // one CTA per SM
 constexpr uint32_t kIdleLimit = 1u << 24;  // rounds without work after which the issuing warp gives up (seconds)
 
@@ -113,7 +112,7 @@ struct Scratch {
   uint32_t *status;
   Split *split;  // [G]
   float2 *ml;    // [2 * G][kH]
-  float *o;      // [2 * G][kH][kD]
+  float4 *o;     // [2 * G][kH / 4][kD], four heads together: as TMEM holds them
 };
 
 // The job list.
@@ -221,15 +220,15 @@ __device__ __forceinline__ void tmem_ld_s(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr));
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; i++) r[i] = __float_as_uint(v[i]);
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -694,16 +693,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (moved && ok) {  // rescale O^T: lane = dim, columns = heads; the last second product is done
         tc::tc_fence_after();
 #pragma unroll 1
-        for (int q = 0; q < 8; q++) {
-          const uint32_t ta = tmem + quarter + kOCol + 32 * q;
-          uint32_t v[32];
-          tc::tmem_ld32_issue(ta, v);
-          tc::tmem_ld_wait();
-          tc::tmem_ld32_pin(v);
+        for (int q = 0; q < 16; q++) {
+          const uint32_t ta = tmem + quarter + kOCol + 16 * q;
+          float v[16];
+          tc::tmem_ld16(ta, v);
 #pragma unroll
-          for (int h = 0; h < 32; h++)
-            v[h] = __float_as_uint(__uint_as_float(v[h]) * sm->alpha[stage][32 * (q & 1) + h]);
-          tmem_st32(ta, v);
+          for (int h = 0; h < 16; h++) v[h] *= sm->alpha[stage][16 * (q & 3) + h];
+          tmem_st16(ta, v);
         }
         tmem_st_wait();
       }
@@ -750,22 +746,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         bar_or(1, 32 * kSoftmaxWarps, 0u);  // sm->l is in
 #pragma unroll 1
-        for (int q = 0; q < 8 && ok; q++) {
-          const int d = 128 * (q >> 1) + 32 * warp + lane, hb = 32 * (q & 1);
-          uint32_t v[32];
-          tc::tmem_ld32_issue(tmem + quarter + kOCol + 32 * q, v);
-          tc::tmem_ld_wait();
-          tc::tmem_ld32_pin(v);
+        for (int q = 0; q < 16 && ok; q++) {  // 16 heads of a dim tile at a time
+          const int d = 128 * (q >> 2) + 32 * warp + lane, hb = 16 * (q & 3);
+          float v[16];
+          tc::tmem_ld16(tmem + quarter + kOCol + 16 * q, v);
           if (out_now) {
-            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + (out_row + hb) * kD + d;
+            // an 8 x 8 exchange among eight lanes: lane = dim, registers = heads, to a lane with eight dims of a head
+            uint32_t w1[8], w2[8], w3[8];
+            const uint32_t pick = (lane & 1) ? 0x3276u : 0x5410u;  // odd: other's high, own high half; even: own low, other's low
 #pragma unroll
-            for (int h = 0; h < 32; h++)
-              if (hb + h < heads) o[h * kD] = __float2bfloat16_rn(__uint_as_float(v[h]) * sm->l[hb + h]);
+            for (int k = 0; k < 8; k++) {
+              const __nv_bfloat162 two =
+                  __floats2bfloat162_rn(v[2 * k] * sm->l[hb + 2 * k], v[2 * k + 1] * sm->l[hb + 2 * k + 1]);
+              const uint32_t own = *reinterpret_cast<const uint32_t *>(&two);
+              w1[k] = __byte_perm(own, __shfl_xor_sync(0xFFFFFFFFu, own, 1), pick);  // head 2k + lane % 2
+            }
+#pragma unroll
+            for (int k = 0; k < 4; k++) {  // head 4k + lane % 4: words 2k, 2k + 1
+              const bool odd = lane & 2;
+              const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? w1[2 * k] : w1[2 * k + 1], 2);
+              w2[2 * k] = odd ? other : w1[2 * k];
+              w2[2 * k + 1] = odd ? w1[2 * k + 1] : other;
+            }
+            uint16_t *o = static_cast<uint16_t *>(a.out) + (out_row + hb + (lane & 7)) * kD + (d & ~7);
+#pragma unroll
+            for (int k = 0; k < 2; k++) {  // head 8k + lane % 8: words 4k .. 4k + 3
+              const bool odd = lane & 4;
+#pragma unroll
+              for (int j = 0; j < 2; j++) {
+                const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? w2[4 * k + j] : w2[4 * k + 2 + j], 4);
+                w3[4 * k + j] = odd ? other : w2[4 * k + j];
+                w3[4 * k + 2 + j] = odd ? w2[4 * k + 2 + j] : other;
+              }
+              if (hb + 8 * k + (lane & 7) < heads)
+                *reinterpret_cast<uint4 *>(o + 8 * k * kD) = make_uint4(w3[4 * k], w3[4 * k + 1], w3[4 * k + 2], w3[4 * k + 3]);
+            }
           } else {
-            float *o = ws.o + (slot_o * kH + hb) * kD + d;
+            float4 *o = ws.o + (slot_o * (kH / 4) + hb / 4) * kD + d;
 #pragma unroll
-            for (int h = 0; h < 32; h++)
-              if (hb + h < heads) o[h * kD] = __uint_as_float(v[h]);
+            for (int k = 0; k < 4; k++) o[k * kD] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
           }
         }
         tc::tc_fence_before();
@@ -786,129 +805,119 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && sm->abort) raise_status(ws.status, LIDX_DEV_TIMEOUT);
 }
 
-// Joins the partial results of jobs that span CTAs.  A job with few partials
-// is 64 items (a head each), one with many 256 (a head and a quarter of its
-// dims): in a CTA of 128 threads, 128 or 32 take four dims each, and one or
-// four groups of them every partial or every fourth.
+__device__ __forceinline__ void join(float &m, float &l, float &acc, float m2, float l2, float v2) {
+  const float mn = fmaxf(m, m2), f = m == mn ? 1.f : exp2_approx(m - mn), e = m2 == mn ? 1.f : exp2_approx(m2 - mn);
+  l = fmaf(l, f, e * l2);
+  acc = fmaf(acc, f, e * v2);
+  m = mn;
+}
+
+// Joins the partial results of jobs that span CTAs.  An item is such a job,
+// four of its heads and 32 of its dims (lane = dim).  Where a job has few
+// partials, as with many short jobs, a warp joins an item by itself; where it
+// has many, the eight warps of the CTA take every eighth partial each and
+// their sums meet in shared memory, where a thread joins one head of a dim.
 __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const lidx_paged_attn_args a, const Jobs jobs,
                                                                          const Scratch ws) {
-  __shared__ Split list[kMaxCtas];
-  __shared__ int32_t base[kMaxCtas + 1];  // first item of each
-  __shared__ int32_t sums[2][kMergeThreads / 32];
-  __shared__ float4 acc_s[kMergeThreads];
-  __shared__ float2 ml_s[kMergeThreads];
+  constexpr int kWarps = kMergeThreads / 32, kItems = (kH / 4) * (kD / 32);
+  __shared__ Split list[kMaxCtas];  // jobs with few partials from the front, with many from the back
+  __shared__ int32_t count[2][kWarps];
+  __shared__ float4 acc_s[kWarps][32], m_s[kWarps], l_s[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   pdl_wait();  // the partial results come from the previous kernel
-  // the split jobs, in the same order in every CTA
-  int n_list = 0, n_items = 0;
-  for (int g0 = 0; g0 < jobs.G; g0 += kMergeThreads) {
-    Split sp;
-    sp.job = -1;
-    if (g0 + tid < jobs.G) sp = ws.split[g0 + tid];
-    int items = 0;
-    if (sp.job >= 0) {
-      const Deal deal(sp.total, jobs.G);
-      items = deal.owner(sp.end - 1) - deal.owner(sp.start) >= kFewPartials ? 4 * kH : kH;
-    }
-    const int incl = warp_inclusive_scan(items), flag = sp.job >= 0 ? 1 : 0;
-    const int rank = warp_inclusive_scan(flag);
-    if (lane == 31) {
-      sums[0][warp] = incl;
-      sums[1][warp] = rank;
-    }
-    __syncthreads();
-    int at_item = n_items + incl - items, at = n_list + rank - flag;
-#pragma unroll
-    for (int w = 0; w < kMergeThreads / 32; w++) {
-      if (w < warp) {
-        at_item += sums[0][w];
-        at += sums[1][w];
-      }
-      n_items += sums[0][w];
-      n_list += sums[1][w];
-    }
-    if (flag) {
-      list[at] = sp;
-      base[at] = at_item;
-    }
-    __syncthreads();
-  }
-  if (tid == 0) base[n_list] = n_items;
-  __syncthreads();
-#pragma unroll 1
-  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-    int lo = 0, hi = n_list - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (base[mid] <= item) lo = mid;
-      else hi = mid - 1;
-    }
-    const Split sp = list[lo];
-    const bool many = base[lo + 1] - base[lo] > kH;
-    const int h = many ? (item - base[lo]) >> 2 : item - base[lo];
-    const int32_t bt = sp.job >> jobs.group_shift, group = sp.job & ((1 << jobs.group_shift) - 1);
-    if (h >= min(kH, a.H - group * kH)) continue;
+  // the split jobs, in the same order in every CTA (kMaxCtas <= kMergeThreads)
+  Split sp;
+  sp.job = -1;
+  if (tid < jobs.G) sp = ws.split[tid];
+  bool many = false;
+  if (sp.job >= 0) {
     const Deal deal(sp.total, jobs.G);
-    const int32_t from = deal.owner(sp.start), last = deal.owner(sp.end - 1);
-    const int d4 = many ? 32 * ((item - base[lo]) & 3) + lane : tid;  // this thread's four dims
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float m = -INFINITY, l = 0.f;
-    const int step = many ? 4 : 1;
+    many = deal.owner(sp.end - 1) - deal.owner(sp.start) >= kWarps;
+  }
+  const uint32_t few_mask = __ballot_sync(0xFFFFFFFFu, sp.job >= 0 && !many), many_mask = __ballot_sync(0xFFFFFFFFu, many);
+  if (lane == 0) {
+    count[0][warp] = __popc(few_mask);
+    count[1][warp] = __popc(many_mask);
+  }
+  __syncthreads();
+  int n_few = 0, n_many = 0, at = __popc((many ? many_mask : few_mask) & ((1u << lane) - 1u));
+#pragma unroll
+  for (int w = 0; w < kWarps; w++) {
+    if (w < warp) at += count[many][w];
+    n_few += count[0][w];
+    n_many += count[1][w];
+  }
+  if (sp.job >= 0) list[many ? kMaxCtas - 1 - at : at] = sp;
+  __syncthreads();
+
+  float m[4], l[4], acc[4];  // of four heads, dim d0 + lane
+  auto gather = [&](const Split &sj, int h4, int d0, int first, int step) {  // every step-th partial of the job
+    const Deal deal(sj.total, jobs.G);
+    const int32_t from = deal.owner(sj.start), last = deal.owner(sj.end - 1);
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      m[k] = -INFINITY;
+      l[k] = acc[k] = 0.f;
+    }
 #pragma unroll 1
-    for (int32_t c0 = from + (many ? warp : 0); c0 <= last; c0 += kBatch * step) {
-      float4 v[kBatch];
-      float2 w[kBatch];
+    for (int32_t c0 = from + first; c0 <= last; c0 += step * kBatch) {
+      float4 v[kBatch], ml[kBatch][2];
 #pragma unroll
       for (int k = 0; k < kBatch; k++) {
-        const int32_t c = c0 + k * step;
-        w[k] = make_float2(-INFINITY, 0.f);
-        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c <= last) {
-          // the job is the CTA's first one unless the CTA began with an earlier job
-          const int32_t slot = 2 * c + (deal.start(c) < sp.start ? 1 : 0);
-          w[k] = ws.ml[slot * kH + h];
-          v[k] = reinterpret_cast<const float4 *>(ws.o + static_cast<size_t>(slot * kH + h) * kD)[d4];
-        }
+        // (a partial beyond the last one: the last one again, not joined below)
+        const int32_t c = min(c0 + k * step, last);
+        // the job is the CTA's first one unless the CTA began with an earlier job
+        const int32_t slot = 2 * c + (deal.start(c) < sj.start ? 1 : 0);
+        const float4 *p = reinterpret_cast<const float4 *>(ws.ml + slot * kH + 4 * h4);
+        ml[k][0] = p[0];
+        ml[k][1] = p[1];
+        v[k] = ws.o[static_cast<size_t>(slot * (kH / 4) + h4) * kD + d0 + lane];
       }
 #pragma unroll
       for (int k = 0; k < kBatch; k++) {
-        if (w[k].x == -INFINITY && w[k].y == 0.f) continue;  // no row of it counts (a NaN sum does)
-        const float mn = fmaxf(m, w[k].x), f = m == mn ? 1.f : exp2f(m - mn), e = w[k].x == mn ? 1.f : exp2f(w[k].x - mn);
-        l = fmaf(l, f, e * w[k].y);
-        acc.x = fmaf(acc.x, f, e * v[k].x);
-        acc.y = fmaf(acc.y, f, e * v[k].y);
-        acc.z = fmaf(acc.z, f, e * v[k].z);
-        acc.w = fmaf(acc.w, f, e * v[k].w);
-        m = mn;
+        if (c0 + k * step > last) break;
+        join(m[0], l[0], acc[0], ml[k][0].x, ml[k][0].y, v[k].x);
+        join(m[1], l[1], acc[1], ml[k][0].z, ml[k][0].w, v[k].y);
+        join(m[2], l[2], acc[2], ml[k][1].x, ml[k][1].y, v[k].z);
+        join(m[3], l[3], acc[3], ml[k][1].z, ml[k][1].w, v[k].w);
       }
     }
-    if (many) {  // the four warps' parts, joined by the first
-      __syncthreads();
-      acc_s[tid] = acc;
-      ml_s[tid] = make_float2(m, l);
-      __syncthreads();
-      if (warp != 0) continue;
-#pragma unroll
-      for (int w = 1; w < 4; w++) {
-        const float2 x = ml_s[32 * w + lane];
-        if (x.x == -INFINITY && x.y == 0.f) continue;
-        const float mn = fmaxf(m, x.x), f = m == mn ? 1.f : exp2f(m - mn), e = x.x == mn ? 1.f : exp2f(x.x - mn);
-        const float4 v = acc_s[32 * w + lane];
-        l = fmaf(l, f, e * x.y);
-        acc.x = fmaf(acc.x, f, e * v.x);
-        acc.y = fmaf(acc.y, f, e * v.y);
-        acc.z = fmaf(acc.z, f, e * v.z);
-        acc.w = fmaf(acc.w, f, e * v.w);
-        m = mn;
-      }
-    }
-    const float il = l == 0.f ? 0.f : 1.f / l;
+  };
+  auto write = [&](const Split &sj, int h, int d0, float M, float Ls, float A) {  // head h of the job's group
+    const int32_t bt = sj.job >> jobs.group_shift, group = sj.job & ((1 << jobs.group_shift) - 1);
+    if (group * kH + h >= a.H) return;
     const int64_t row = static_cast<int64_t>(bt) * a.H + group * kH + h;
-    const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * il, acc.y * il), y = __floats2bfloat162_rn(acc.z * il, acc.w * il);
-    reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * kD)[d4] =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
-    if (a.lse && d4 == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    static_cast<__nv_bfloat16 *>(a.out)[row * kD + d0 + lane] = __float2bfloat16_rn(A * (Ls == 0.f ? 0.f : 1.f / Ls));
+    if (a.lse && d0 == 0 && lane == 0) a.lse[row] = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * kLn2;
+  };
+#pragma unroll 1
+  for (int item = blockIdx.x * kWarps + warp; item < n_few * kItems; item += gridDim.x * kWarps) {
+    const Split sj = list[item / kItems];
+    const int h4 = (item % kItems) / (kD / 32), d0 = 32 * (item % (kD / 32));
+    gather(sj, h4, d0, 0, 1);
+#pragma unroll
+    for (int k = 0; k < 4; k++) write(sj, 4 * h4 + k, d0, m[k], l[k], acc[k]);
+  }
+#pragma unroll 1
+  for (int item = blockIdx.x; item < n_many * kItems; item += gridDim.x) {
+    const Split sj = list[kMaxCtas - 1 - item / kItems];
+    const int h4 = (item % kItems) / (kD / 32), d0 = 32 * (item % (kD / 32));
+    gather(sj, h4, d0, warp, kWarps);
+    __syncthreads();
+    acc_s[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    if (lane == 0) {
+      m_s[warp] = make_float4(m[0], m[1], m[2], m[3]);
+      l_s[warp] = make_float4(l[0], l[1], l[2], l[3]);
+    }
+    __syncthreads();
+    if (warp >= 4) continue;  // warp k < 4 finishes head k
+    float M = -INFINITY, Ls = 0.f, A = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; w++)
+      join(M, Ls, A, reinterpret_cast<const float *>(&m_s[w])[warp], reinterpret_cast<const float *>(&l_s[w])[warp],
+           reinterpret_cast<const float *>(&acc_s[w][lane])[warp]);
+    write(sj, 4 * h4 + warp, d0, M, Ls, A);
   }
 }
 
@@ -973,7 +982,7 @@ cudaError_t launch_paged_attn(const lidx_paged_attn_args &a, void *ws, cudaStrea
   p += align256(j.G * sizeof(Split));
   s.ml = reinterpret_cast<float2 *>(p);
   p += static_cast<size_t>(j.G) * 2 * kH * 8;
-  s.o = reinterpret_cast<float *>(p);
+  s.o = reinterpret_cast<float4 *>(p);
   CUtensorMap tm;
   if (!make_tmap_3d(&tm, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kD, a.H, static_cast<uint64_t>(a.B) * a.T, 64, kH,
                     CU_TENSOR_MAP_SWIZZLE_128B))
@@ -985,7 +994,7 @@ cudaError_t launch_paged_attn(const lidx_paged_attn_args &a, void *ws, cudaStrea
     default: e = launch<LIDX_BF16>(tm, a, j, s, st); break;
   }
   if (e != cudaSuccess) return e;
-  return launch_kernel(paged_attn_merge_kernel, dim3(8 * sm_count()), dim3(kMergeThreads), 0, st, true, a, j, s);
+  return launch_kernel(paged_attn_merge_kernel, dim3(4 * sm_count()), dim3(kMergeThreads), 0, st, true, a, j, s);
 }
 
 }  // namespace lidx
