@@ -66,7 +66,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 32.f;            // base-2 headroom of the reference maximum
 constexpr int kMergeThreads = 256;
-constexpr int kBatch = 4;                // partials of a warp whose loads are in flight together
+constexpr int kFew = 8;                  // partials that one warp joins
 constexpr int kMaxCtas = 256;            // one CTA per SM
 constexpr uint32_t kIdleLimit = 1u << 24;  // rounds without work after which the issuing warp gives up (seconds)
 
@@ -805,24 +805,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && sm->abort) raise_status(ws.status, LIDX_DEV_TIMEOUT);
 }
 
-__device__ __forceinline__ void join(float &m, float &l, float &acc, float m2, float l2, float v2) {
-  const float mn = fmaxf(m, m2), f = m == mn ? 1.f : exp2_approx(m - mn), e = m2 == mn ? 1.f : exp2_approx(m2 - mn);
-  l = fmaf(l, f, e * l2);
-  acc = fmaf(acc, f, e * v2);
-  m = mn;
-}
+// A partial's weight and its part of the sum, given the joint maximum M.
+__device__ __forceinline__ float weight_of(float m, float M) { return m == M ? 1.f : exp2_approx(m - M); }
 
 // Joins the partial results of jobs that span CTAs.  An item is such a job,
-// four of its heads and 32 of its dims (lane = dim).  Where a job has few
-// partials, as with many short jobs, a warp joins an item by itself; where it
-// has many, the eight warps of the CTA take every eighth partial each and
-// their sums meet in shared memory, where a thread joins one head of a dim.
+// four of its heads and 32 or 128 of its dims (lane = dim).  First the partials'
+// weights are found, a thread for each partial, then the weighted sum runs
+// over the partials.  Where a job has few of them, as with many short jobs, a
+// warp joins an item by itself; where it has many, the eight warps of the CTA
+// take every eighth partial each and their sums meet in shared memory.
 __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const lidx_paged_attn_args a, const Jobs jobs,
                                                                          const Scratch ws) {
   constexpr int kWarps = kMergeThreads / 32, kItems = (kH / 4) * (kD / 32);
   __shared__ Split list[kMaxCtas];  // jobs with few partials from the front, with many from the back
   __shared__ int32_t count[2][kWarps];
-  __shared__ float4 acc_s[kWarps][32], m_s[kWarps], l_s[kWarps];
+  __shared__ float4 weight_s[kMaxCtas], acc_s[kWarps][32], red_s[2][kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   pdl_wait();  // the partial results come from the previous kernel
@@ -833,7 +830,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const l
   bool many = false;
   if (sp.job >= 0) {
     const Deal deal(sp.total, jobs.G);
-    many = deal.owner(sp.end - 1) - deal.owner(sp.start) >= kWarps;
+    many = deal.owner(sp.end - 1) - deal.owner(sp.start) >= kFew;
   }
   const uint32_t few_mask = __ballot_sync(0xFFFFFFFFu, sp.job >= 0 && !many), many_mask = __ballot_sync(0xFFFFFFFFu, many);
   if (lane == 0) {
@@ -851,73 +848,109 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const l
   if (sp.job >= 0) list[many ? kMaxCtas - 1 - at : at] = sp;
   __syncthreads();
 
-  float m[4], l[4], acc[4];  // of four heads, dim d0 + lane
-  auto gather = [&](const Split &sj, int h4, int d0, int first, int step) {  // every step-th partial of the job
-    const Deal deal(sj.total, jobs.G);
-    const int32_t from = deal.owner(sj.start), last = deal.owner(sj.end - 1);
+  float m[4], l[4], e[4];  // of four heads of the partial that the thread looks after
+  auto look = [&](const float2 *ml) {
 #pragma unroll
     for (int k = 0; k < 4; k++) {
       m[k] = -INFINITY;
-      l[k] = acc[k] = 0.f;
+      l[k] = 0.f;
     }
-#pragma unroll 1
-    for (int32_t c0 = from + first; c0 <= last; c0 += step * kBatch) {
-      float4 v[kBatch], ml[kBatch][2];
-#pragma unroll
-      for (int k = 0; k < kBatch; k++) {
-        // (a partial beyond the last one: the last one again, not joined below)
-        const int32_t c = min(c0 + k * step, last);
-        // the job is the CTA's first one unless the CTA began with an earlier job
-        const int32_t slot = 2 * c + (deal.start(c) < sj.start ? 1 : 0);
-        const float4 *p = reinterpret_cast<const float4 *>(ws.ml + slot * kH + 4 * h4);
-        ml[k][0] = p[0];
-        ml[k][1] = p[1];
-        v[k] = ws.o[static_cast<size_t>(slot * (kH / 4) + h4) * kD + d0 + lane];
-      }
-#pragma unroll
-      for (int k = 0; k < kBatch; k++) {
-        if (c0 + k * step > last) break;
-        join(m[0], l[0], acc[0], ml[k][0].x, ml[k][0].y, v[k].x);
-        join(m[1], l[1], acc[1], ml[k][0].z, ml[k][0].w, v[k].y);
-        join(m[2], l[2], acc[2], ml[k][1].x, ml[k][1].y, v[k].z);
-        join(m[3], l[3], acc[3], ml[k][1].z, ml[k][1].w, v[k].w);
-      }
+    if (ml) {
+      const float4 x = reinterpret_cast<const float4 *>(ml)[0], y = reinterpret_cast<const float4 *>(ml)[1];
+      m[0] = x.x; l[0] = x.y; m[1] = x.z; l[1] = x.w;
+      m[2] = y.x; l[2] = y.y; m[3] = y.z; l[3] = y.w;
     }
   };
-  auto write = [&](const Split &sj, int h, int d0, float M, float Ls, float A) {  // head h of the job's group
+  // the job is the CTA's first one unless the CTA began with an earlier job
+  auto slot_of = [&](const Deal &deal, int32_t c, int32_t start) { return 2 * c + (deal.start(c) < start ? 1 : 0); };
+  auto write = [&](const Split &sj, int h, int d0, float M, float L, float A) {  // head h of the job's group
     const int32_t bt = sj.job >> jobs.group_shift, group = sj.job & ((1 << jobs.group_shift) - 1);
     if (group * kH + h >= a.H) return;
     const int64_t row = static_cast<int64_t>(bt) * a.H + group * kH + h;
-    static_cast<__nv_bfloat16 *>(a.out)[row * kD + d0 + lane] = __float2bfloat16_rn(A * (Ls == 0.f ? 0.f : 1.f / Ls));
-    if (a.lse && d0 == 0 && lane == 0) a.lse[row] = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * kLn2;
+    static_cast<__nv_bfloat16 *>(a.out)[row * kD + d0 + lane] = __float2bfloat16_rn(A * (L == 0.f ? 0.f : 1.f / L));
+    if (a.lse && d0 == 0 && lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
   };
+
 #pragma unroll 1
-  for (int item = blockIdx.x * kWarps + warp; item < n_few * kItems; item += gridDim.x * kWarps) {
-    const Split sj = list[item / kItems];
-    const int h4 = (item % kItems) / (kD / 32), d0 = 32 * (item % (kD / 32));
-    gather(sj, h4, d0, 0, 1);
+  for (int item = blockIdx.x * kWarps + warp; item < n_few * kItems / 4; item += gridDim.x * kWarps) {  // 128 dims each
+    const Split sj = list[item / (kItems / 4)];
+    const int h4 = (item % (kItems / 4)) / 4, d0 = 128 * (item % 4);
+    const Deal deal(sj.total, jobs.G);
+    const int32_t from = deal.owner(sj.start), last = deal.owner(sj.end - 1);
+    float M[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, L[4] = {0.f, 0.f, 0.f, 0.f}, A[4][4] = {};
+#pragma unroll 1
+    for (int32_t c = from; c <= last; c++) {
+      look(ws.ml + slot_of(deal, c, sj.start) * kH + 4 * h4);
 #pragma unroll
-    for (int k = 0; k < 4; k++) write(sj, 4 * h4 + k, d0, m[k], l[k], acc[k]);
+      for (int k = 0; k < 4; k++) M[k] = fmaxf(M[k], m[k]);
+    }
+#pragma unroll 2
+    for (int32_t c = from; c <= last; c++) {
+      const int32_t slot = slot_of(deal, c, sj.start);
+      look(ws.ml + slot * kH + 4 * h4);
+      float4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) v[j] = ws.o[static_cast<size_t>(slot * (kH / 4) + h4) * kD + d0 + 32 * j + lane];
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        const float e0 = weight_of(m[k], M[k]);
+        L[k] = fmaf(e0, l[k], L[k]);
+#pragma unroll
+        for (int j = 0; j < 4; j++) A[k][j] = fmaf(e0, reinterpret_cast<const float *>(&v[j])[k], A[k][j]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) write(sj, 4 * h4 + k, d0 + 32 * j, M[k], L[k], A[k][j]);
   }
+
 #pragma unroll 1
   for (int item = blockIdx.x; item < n_many * kItems; item += gridDim.x) {
     const Split sj = list[kMaxCtas - 1 - item / kItems];
     const int h4 = (item % kItems) / (kD / 32), d0 = 32 * (item % (kD / 32));
-    gather(sj, h4, d0, warp, kWarps);
+    const Deal deal(sj.total, jobs.G);
+    const int32_t from = deal.owner(sj.start), n = deal.owner(sj.end - 1) - from + 1;  // <= kMaxCtas
+    look(tid < n ? ws.ml + slot_of(deal, from + tid, sj.start) * kH + 4 * h4 : nullptr);
+    float M[4], L[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) M[k] = warp_max(m[k]);
+    if (lane == 0) red_s[0][warp] = make_float4(M[0], M[1], M[2], M[3]);
     __syncthreads();
-    acc_s[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    if (lane == 0) {
-      m_s[warp] = make_float4(m[0], m[1], m[2], m[3]);
-      l_s[warp] = make_float4(l[0], l[1], l[2], l[3]);
-    }
-    __syncthreads();
-    if (warp >= 4) continue;  // warp k < 4 finishes head k
-    float M = -INFINITY, Ls = 0.f, A = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; w++)
-      join(M, Ls, A, reinterpret_cast<const float *>(&m_s[w])[warp], reinterpret_cast<const float *>(&l_s[w])[warp],
-           reinterpret_cast<const float *>(&acc_s[w][lane])[warp]);
-    write(sj, 4 * h4 + warp, d0, M, Ls, A);
+#pragma unroll
+      for (int k = 0; k < 4; k++) M[k] = fmaxf(M[k], reinterpret_cast<const float *>(&red_s[0][w])[k]);
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      e[k] = tid < n ? weight_of(m[k], M[k]) : 0.f;
+      L[k] = warp_sum(tid < n ? e[k] * l[k] : 0.f);
+    }
+    if (tid < n) weight_s[tid] = make_float4(e[0], e[1], e[2], e[3]);
+    if (lane == 0) red_s[1][warp] = make_float4(L[0], L[1], L[2], L[3]);
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int32_t c = warp; c < n; c += kWarps) {
+      const float4 v = ws.o[static_cast<size_t>(slot_of(deal, from + c, sj.start) * (kH / 4) + h4) * kD + d0 + lane];
+      const float4 w = weight_s[c];
+      acc.x = fmaf(w.x, v.x, acc.x);
+      acc.y = fmaf(w.y, v.y, acc.y);
+      acc.z = fmaf(w.z, v.z, acc.z);
+      acc.w = fmaf(w.w, v.w, acc.w);
+    }
+    acc_s[warp][lane] = acc;
+    __syncthreads();
+    if (warp < 4) {  // warp k finishes head k
+      float A = 0.f, Ls = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; w++) {
+        A += reinterpret_cast<const float *>(&acc_s[w][lane])[warp];
+        Ls += reinterpret_cast<const float *>(&red_s[1][w])[warp];
+      }
+      write(sj, 4 * h4 + warp, d0, warp == 0 ? M[0] : warp == 1 ? M[1] : warp == 2 ? M[2] : M[3], Ls, A);
+    }
+    __syncthreads();
   }
 }
 
