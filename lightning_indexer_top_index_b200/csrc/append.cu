@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const lidx_append_args
   for (int o = 1; o < 8; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
   if (a.cache.dtype == LIDX_E4M3 && d0 < dim - 64) {
     const int e = am > 0.f ? block_exponent_e4m3(am) : 0;
-    const float inv = ldexpf(1.f, -e);  // exact power of two (e <= 120 for finite fp32 amax)
+    const float inv = inverse_scale(e);  // exact power of two (e <= 120 for finite fp32 amax)
     float s[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) s[i] = v[i] * inv;

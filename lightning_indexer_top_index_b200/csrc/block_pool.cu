@@ -3,7 +3,7 @@
 //
 // One CTA of four warps takes a block at a time.  A warp's loads are 16 bytes a
 // lane of one plane: a row's RoPE dims (or a whole bf16 / fp32 row) take 8 (16,
-// 32) lanes, its E4M3 codes 4, its E2M1 codes 2; the loads of 64 rows are
+// 32) lanes, its E4M3 codes 4, its E2M1 codes 4 of 8 bytes; the loads of 64 rows are
 // dealt out to the warps and are all in flight before the first is used.  A
 // lane sums its dims over its rows in 64 bits, the lanes that hold the same
 // dims add up by halves (each step sends one half and keeps the other), the
@@ -33,24 +33,11 @@ __device__ __forceinline__ double field_double(uint32_t x) {
   return __hiloint2double(static_cast<int>((static_cast<int32_t>(x) >> kShift) & kMask), 0);
 }
 
-// A plane whose rows take kLanes lanes of kBytes bytes, kDims dims each.
+// Dims of a lane's load of a plane, and its bytes (a bf16 plane is also the RoPE dims').
 template <int kFmt>
-struct Plane;
-template <>
-struct Plane<LIDX_F32> {
-  static constexpr int kLanes = 32, kDims = 4, kBytes = 16;
-};
-template <>
-struct Plane<LIDX_BF16> {  // also the RoPE plane, with 8 lanes
-  static constexpr int kLanes = 16, kDims = 8, kBytes = 16;
-};
-template <>
-struct Plane<LIDX_E4M3> {
-  static constexpr int kLanes = 4, kDims = 16, kBytes = 16;
-};
-template <>
-struct Plane<LIDX_E2M1> {
-  static constexpr int kLanes = 4, kDims = 16, kBytes = 8;
+struct Plane {
+  static constexpr int kDims = kFmt == LIDX_F32 ? 4 : kFmt == LIDX_BF16 ? 8 : 16;
+  static constexpr int kBytes = kFmt == LIDX_E2M1 ? 8 : 16;
 };
 
 // s += the dims in w, times their block's factor; `bad` notices what is not finite
@@ -188,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) block_pool_kernel(const lidx_block_p
     const uint8_t *data = static_cast<const uint8_t *>(kv.data);
     bool bad;
     if constexpr (kFmt == LIDX_F32 || kFmt == LIDX_BF16) {
-      bad = sum_plane<kFmt, Plane<kFmt>::kLanes>(data, kv.ld * (kFmt == LIDX_F32 ? 4 : 2), nullptr, 0, p0, count, sums[warp]);
+      bad = sum_plane<kFmt, 128 / Plane<kFmt>::kDims>(data, kv.ld * (kFmt == LIDX_F32 ? 4 : 2), nullptr, 0, p0, count, sums[warp]);
     } else {
       bad = sum_plane<kFmt, 4>(data, kv.ld, kv.scale, kv.ld_scale, p0, count, sums[warp]);
       bad |= sum_plane<LIDX_BF16, 8>(static_cast<const uint8_t *>(kv.rope), 2 * kv.ld_rope, nullptr, 0, p0, count,

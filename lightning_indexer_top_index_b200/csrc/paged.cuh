@@ -87,49 +87,66 @@ struct E2m1Scale {
 __device__ __forceinline__ float bf16x2_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16x2_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// Values of dims [8t, 8t + 8) of pool row p as fp32, the exact products of
-// code and scale.
-__device__ __forceinline__ void load8(const lidx_kv &kv, int64_t p, int t, float (&v)[8]) {
-  const int d0 = 8 * t, q = kv.dim - 64;
-  if (kv.dtype == LIDX_F32) {
-    const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(kv.data) + p * kv.ld + d0);
-    const float4 a = __ldg(s), b = __ldg(s + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    return;
+// Dims [8t, 8t + 8) of a pool row: loaded first, made values (the exact
+// products of code and scale, as fp32) later, so that many loads are in flight.
+template <int kFmt>
+struct Dims8 {
+  uint4 w[kFmt == LIDX_F32 ? 2 : 1];
+  uint32_t scale;
+  bool codes;  // E4M3 or E2M1 codes, not 16- or 32-bit values
+
+  __device__ __forceinline__ void load(const lidx_kv &kv, int64_t p, int t) {
+    const int d0 = 8 * t, q = kv.dim - 64;
+    codes = (kFmt == LIDX_E4M3 || kFmt == LIDX_E2M1) && d0 < q;
+    if (kFmt == LIDX_F32) {
+      const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const float *>(kv.data) + p * kv.ld + d0);
+      w[0] = __ldg(s);
+      w[kFmt == LIDX_F32] = __ldg(s + 1);
+    } else if (!codes) {
+      const uint16_t *s = kFmt == LIDX_BF16 ? static_cast<const uint16_t *>(kv.data) + p * kv.ld + d0
+                                            : static_cast<const uint16_t *>(kv.rope) + p * kv.ld_rope + (d0 - q);
+      w[0] = __ldg(reinterpret_cast<const uint4 *>(s));
+    } else {
+      const uint8_t *data = static_cast<const uint8_t *>(kv.data) + p * kv.ld;
+      if (kFmt == LIDX_E4M3) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(data + d0));
+        w[0].x = x.x;
+        w[0].y = x.y;
+      } else {
+        w[0].x = __ldg(reinterpret_cast<const uint32_t *>(data + d0 / 2));
+      }
+      scale = __ldg(kv.scale + p * kv.ld_scale + d0 / (kFmt == LIDX_E4M3 ? 64 : 32));
+    }
   }
-  if (kv.dtype == LIDX_BF16 || d0 >= q) {
-    const uint16_t *s = kv.dtype == LIDX_BF16 ? static_cast<const uint16_t *>(kv.data) + p * kv.ld + d0
-                                              : static_cast<const uint16_t *>(kv.rope) + p * kv.ld_rope + (d0 - q);
-    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(s));
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    if (kFmt == LIDX_F32) {
+      const uint4 &y = w[kFmt == LIDX_F32];
+      v[0] = __uint_as_float(w[0].x); v[1] = __uint_as_float(w[0].y);
+      v[2] = __uint_as_float(w[0].z); v[3] = __uint_as_float(w[0].w);
+      v[4] = __uint_as_float(y.x); v[5] = __uint_as_float(y.y);
+      v[6] = __uint_as_float(y.z); v[7] = __uint_as_float(y.w);
+      return;
+    }
+    uint32_t x[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+    float s = 1.f;
+    if (codes) {
+      if (kFmt == LIDX_E4M3) {
+        x[3] = e4m3x2_to_bf16x2(x[1] >> 16);
+        x[2] = e4m3x2_to_bf16x2(x[1]);
+        x[1] = e4m3x2_to_bf16x2(x[0] >> 16);
+        x[0] = e4m3x2_to_bf16x2(x[0]);
+      } else {
+        e2m1x8_to_bf16x2(w[0].x, x);
+      }
+      s = e8m0_to_f32(scale);
+    }
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      v[2 * i] = bf16x2_lo(x[i]);
-      v[2 * i + 1] = bf16x2_hi(x[i]);
+      v[2 * i] = bf16x2_lo(x[i]) * s;
+      v[2 * i + 1] = bf16x2_hi(x[i]) * s;
     }
-    return;
   }
-  const uint8_t *data = static_cast<const uint8_t *>(kv.data);
-  uint32_t x[4];
-  float s;
-  if (kv.dtype == LIDX_E4M3) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(data + p * kv.ld + d0));
-    s = e8m0_to_f32(__ldg(kv.scale + p * kv.ld_scale + d0 / 64));
-    x[0] = e4m3x2_to_bf16x2(w.x);
-    x[1] = e4m3x2_to_bf16x2(w.x >> 16);
-    x[2] = e4m3x2_to_bf16x2(w.y);
-    x[3] = e4m3x2_to_bf16x2(w.y >> 16);
-  } else {
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(data + p * kv.ld + d0 / 2));
-    s = e8m0_to_f32(__ldg(kv.scale + p * kv.ld_scale + d0 / 32));
-    e2m1x8_to_bf16x2(w, x);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    v[2 * i] = bf16x2_lo(x[i]) * s;
-    v[2 * i + 1] = bf16x2_hi(x[i]) * s;
-  }
-}
+};
 
 }  // namespace lidx

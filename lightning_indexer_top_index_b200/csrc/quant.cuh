@@ -6,16 +6,19 @@
 namespace lidx {
 
 // smallest e in [-127, 127] with amax <= top * 2^e (amax finite, > 0), for a
-// format whose largest value is top = frac * 2^ex_top with frac in [0.5, 1):
-// with amax = f * 2^ex, amax <= top * 2^e holds from e = ex - ex_top on when
-// f <= frac, else one later.  E4M3: 448 = 0.875 * 2^9; E2M1: 6 = 0.75 * 2^3.
-__device__ __forceinline__ int block_exponent(float amax, float frac, int ex_top) {
-  int ex;
-  const float f = frexpf(amax, &ex);
-  return max(-127, min(127, ex - ex_top + (f > frac ? 1 : 0)));
+// format whose largest value is top = m * 2^ex_top with m in [1, 2), given as
+// m's mantissa bits: amax = m' * 2^x needs e = x - ex_top when m' <= m, else
+// one more (a subnormal amax is below top * 2^-127 for both formats).
+// E4M3: 448 = 1.75 * 2^8; E2M1: 6 = 1.5 * 2^2.
+__device__ __forceinline__ int block_exponent(float amax, uint32_t mantissa, int ex_top) {
+  const uint32_t u = __float_as_uint(amax);
+  return max(-127, static_cast<int>(u >> 23) - 127 - ex_top + ((u & 0x7FFFFFu) > mantissa ? 1 : 0));
 }
-__device__ __forceinline__ int block_exponent_e4m3(float amax) { return block_exponent(amax, 0.875f, 9); }
-__device__ __forceinline__ int block_exponent_e2m1(float amax) { return block_exponent(amax, 0.75f, 3); }
+__device__ __forceinline__ int block_exponent_e4m3(float amax) { return block_exponent(amax, 0x600000u, 8); }
+__device__ __forceinline__ int block_exponent_e2m1(float amax) { return block_exponent(amax, 0x400000u, 2); }
+
+// 2^-e, exactly, for e in [-127, 126] (the exponents of finite magnitudes)
+__device__ __forceinline__ float inverse_scale(int e) { return __uint_as_float(static_cast<uint32_t>(127 - e) << 23); }
 
 __device__ __forceinline__ uint32_t e4m3x2(float hi, float lo) {
   uint16_t r;
@@ -42,13 +45,9 @@ __device__ __forceinline__ uint32_t pack4_e4m3(const float *v) {
   return r;
 }
 
-// Eight E2M1 codes of v already divided by its block scale, v[0] in the low
-// nibble: the nearest value (ties to the even code), |v| > 6 saturating, NaN
-// as +6.
-__device__ __forceinline__ uint32_t pack8_e2m1(const float *v) {
-  float s[8];
-#pragma unroll
-  for (int i = 0; i < 8; i++) s[i] = is_nan_bits(v[i]) ? 6.f : v[i];
+// Eight E2M1 codes of finite v already divided by its block scale, v[0] in the
+// low nibble: the nearest value (ties to the even code), |v| > 6 saturating.
+__device__ __forceinline__ uint32_t pack8_e2m1_finite(const float *s) {
   uint32_t r;
   asm("{\n"
       " .reg .b8 a, b, c, d;\n"
@@ -61,6 +60,19 @@ __device__ __forceinline__ uint32_t pack8_e2m1(const float *v) {
       : "=r"(r)
       : "f"(s[0]), "f"(s[1]), "f"(s[2]), "f"(s[3]), "f"(s[4]), "f"(s[5]), "f"(s[6]), "f"(s[7]));
   return r;
+}
+
+// The same for any v: NaN as +6, infinities saturating.
+__device__ __forceinline__ uint32_t pack8_e2m1(const float *v) {
+  float s[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) s[i] = is_nan_bits(v[i]) ? 6.f : v[i];
+  return pack8_e2m1_finite(s);
+}
+
+// Four E4M3 codes of v with |v| <= 448.
+__device__ __forceinline__ uint32_t pack4_e4m3_in_range(const float *v) {
+  return e4m3x2(v[1], v[0]) | (e4m3x2(v[3], v[2]) << 16);
 }
 
 // bf16 bits of x, nearest even; NaN keeps its payload's top bits, quieted
