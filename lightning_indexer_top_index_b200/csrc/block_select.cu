@@ -11,9 +11,12 @@
 // dot becomes a double by its bits (2^52 + n, minus 2^52), which costs an add.
 //
 // Selection.  Scores become order-preserving 64-bit keys in shared memory
-// (0: not eligible, all ones: always taken); the k-th largest is found by
-// radix over 11-bit digits from the highest bit in which the keys differ,
-// until the digit that holds it has few keys, which are ranked directly.  Ids
+// (0: not eligible, all ones: always taken).  Few keys are ranked directly, a
+// thread each.  More are binned linearly in value between the smallest and the
+// largest score (the bin is a monotone function of the score, so the bin that
+// holds the k-th largest and the count above it are exact), and the keys of
+// that bin are ranked; where too many share it, a radix over 11-bit digits
+// from the highest bit in which the keys differ finds the k-th largest.  Ids
 // come out ascending by a prefix sum; equal keys are taken from the lowest
 // index on.
 //
@@ -36,7 +39,8 @@ constexpr int kMaxCluster = 8;
 constexpr int kMaxSlice = 16384;  // keys a CTA holds
 constexpr int kMaxK = 256;
 constexpr int kDigit = 11, kBins = 1 << kDigit;
-constexpr int kCand = 256;        // keys ranked directly
+constexpr int kCand = 256;        // keys of a bin ranked directly
+constexpr int kDirect = 128;      // keys of a row ranked directly without binning
 constexpr int kPitch = 144;       // bytes between a head's codes: 16-byte reads of 8 heads x 4 lanes hit all banks
 constexpr uint64_t kForced = ~0ull;
 
@@ -48,6 +52,9 @@ struct Smem {
   uint64_t red_or[kWarps], red_and[kWarps];
   uint32_t scan_a[kWarps], scan_b[kWarps];
   uint32_t n_cand, bin, above, bin_count;
+  float red_lo[kWarps], red_hi[kWarps];
+  uint32_t red_some[kWarps], red_must[kWarps];
+  int32_t picked[kMaxK];
   uint64_t threshold;
   uint32_t need;
   // the first CTA's side of the exchange
@@ -112,12 +119,61 @@ __device__ __forceinline__ void scan2(Smem &sm, uint32_t x, uint32_t y, uint32_t
   }
 }
 
-// The k-th largest (k >= 1) of those of the n keys that are neither 0 nor
-// kForced, of which there are `count` > k: sm.threshold, and in sm.need how
-// many keys equal to it belong to the k largest.
 __device__ __forceinline__ bool ranked(uint64_t key) { return key + 1ull > 1ull; }  // neither 0 nor kForced
 
-__device__ void kth_largest(Smem &sm, const uint64_t *keys, int n, uint32_t count, uint32_t k) {
+__device__ __forceinline__ float value_of(uint64_t key) {  // monotone in the key
+  const uint64_t u = (key >> 63) ? key & 0x7FFFFFFFFFFFFFFFull : ~key;
+  return static_cast<float>(__longlong_as_double(static_cast<long long>(u)));
+}
+
+// The bin that holds the want-th largest of sm.hist's `bins` counted keys,
+// from above: sm.bin, sm.above (keys in the bins above it), sm.bin_count.
+__device__ __forceinline__ void find_bin(Smem &sm, uint32_t want) {
+  const int tid = threadIdx.x, per = kBins / kThreads;  // thread t sums bins from the top on
+  uint32_t mine = 0;
+#pragma unroll
+  for (int i = 0; i < per; i++) mine += sm.hist[kBins - 1 - (tid * per + i)];
+  uint32_t before, zero, total, zero2;
+  scan2(sm, mine, 0u, before, zero, total, zero2);
+  if (before < want && want <= before + mine) {
+    uint32_t at = before;
+    for (int i = 0; i < per; i++) {
+      const int bin = kBins - 1 - (tid * per + i);
+      const uint32_t h = sm.hist[bin];
+      if (want <= at + h) {
+        sm.bin = bin;
+        sm.above = at;
+        sm.bin_count = h;
+        break;
+      }
+      at += h;
+    }
+  }
+  __syncthreads();
+}
+
+// The want-th largest of the sm.n_cand <= kCand keys in sm.cand: sm.threshold,
+// and in sm.need how many keys equal to it belong to the `want` largest.
+__device__ __forceinline__ void rank_candidates(Smem &sm, uint32_t want) {
+  const int tid = threadIdx.x, nc = sm.n_cand;
+  if (tid < nc) {
+    const uint64_t x = sm.cand[tid];
+    uint32_t above = 0, same = 0;
+    for (int i = 0; i < nc; i++) {
+      above += sm.cand[i] > x;
+      same += sm.cand[i] == x;
+    }
+    if (above < want && want <= above + same) {  // all threads with this value write the same
+      sm.threshold = x;
+      sm.need = want - above;
+    }
+  }
+  __syncthreads();
+}
+
+// The k-th largest (k >= 1) of those of the n keys that are neither 0 nor
+// kForced, of which there are `count` > k, by radix: sm.threshold and sm.need.
+__device__ __noinline__ void kth_by_radix(Smem &sm, const uint64_t *keys, int n, uint32_t count, uint32_t k) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint64_t any = 0ull, all = ~0ull;
   for (int i = tid; i < n; i += kThreads) {
@@ -154,31 +210,11 @@ __device__ void kth_largest(Smem &sm, const uint64_t *keys, int n, uint32_t coun
     __syncthreads();
     for (int i = tid; i < n; i += kThreads) {
       const uint64_t x = keys[i];
-      if (ranked(x) && (top == 64 || (x >> top) == prefix)) atomicAdd(&sm.hist[static_cast<uint32_t>(x >> shift) & (bins - 1)], 1u);
+      if (ranked(x) && (top == 64 || (x >> top) == prefix))
+        atomicAdd(&sm.hist[static_cast<uint32_t>(x >> shift) & (bins - 1)], 1u);
     }
     __syncthreads();
-    // bin holding rank `want` from above: thread t sums bins [8t', 8t' + 8) with t' counted from the top
-    const int per = kBins / kThreads;
-    uint32_t mine = 0;
-#pragma unroll
-    for (int i = 0; i < per; i++) mine += sm.hist[kBins - 1 - (tid * per + i)];
-    uint32_t before, dummy, tot, dummy2;
-    scan2(sm, mine, 0u, before, dummy, tot, dummy2);
-    if (before < want && want <= before + mine) {
-      uint32_t at = before;
-      for (int i = 0; i < per; i++) {
-        const int bin = kBins - 1 - (tid * per + i);
-        const uint32_t h = sm.hist[bin];
-        if (want <= at + h) {
-          sm.bin = bin;
-          sm.above = at;
-          sm.bin_count = h;
-          break;
-        }
-        at += h;
-      }
-    }
-    __syncthreads();
+    find_bin(sm, want);
     prefix = (top == 64 ? 0ull : prefix << (top - shift)) | sm.bin;
     want -= sm.above;
     count = sm.bin_count;
@@ -200,42 +236,82 @@ __device__ void kth_largest(Smem &sm, const uint64_t *keys, int n, uint32_t coun
     if (ranked(x) && (top == 64 || (x >> top) == prefix)) sm.cand[atomicAdd(&sm.n_cand, 1u)] = x;
   }
   __syncthreads();
-  const int nc = sm.n_cand;  // == count <= kCand
-  if (tid < nc) {
-    const uint64_t x = sm.cand[tid];
-    uint32_t above = 0, same = 0;
-    for (int i = 0; i < nc; i++) {
-      above += sm.cand[i] > x;
-      same += sm.cand[i] == x;
-    }
-    if (above < want && want <= above + same) {  // all threads with this value write the same
-      sm.threshold = x;
-      sm.need = want - above;
-    }
-  }
-  __syncthreads();
+  rank_candidates(sm, want);
 }
 
-// Calls emit(slot, i) for the k largest of keys[0..n) (ties to the lower i),
-// slots 0.. in ascending i; returns how many there are.
-template <typename Emit>
-__device__ int select_k(Smem &sm, const uint64_t *keys, int n, int k, Emit emit) {
+// The same, with the scores binned linearly between lo and hi first.
+__device__ __forceinline__ void kth_largest(Smem &sm, const uint64_t *keys, int n, uint32_t count, uint32_t k, float lo,
+                                            float hi) {
   const int tid = threadIdx.x;
-  uint32_t some = 0, must = 0;
-  for (int i = tid; i < n; i += kThreads) {
-    some += keys[i] != 0ull;
-    must += keys[i] == kForced;
+  // infinities, NaN ranges and equal scores: everything in bin 0
+  float per_bin = (kBins - 1) / (hi - lo);
+  if (!(per_bin < 3e38f) || !(hi - lo < 3e38f)) per_bin = 0.f;
+  auto bin_of = [&](uint64_t key) {
+    return min(max(static_cast<int>((value_of(key) - lo) * per_bin), 0), kBins - 1);
+  };
+  for (int i = tid; i < kBins; i += kThreads) sm.hist[i] = 0u;
+  if (tid == 0) sm.n_cand = 0u;
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads)
+    if (ranked(keys[i])) atomicAdd(&sm.hist[bin_of(keys[i])], 1u);
+  __syncthreads();
+  find_bin(sm, k);
+  if (sm.bin_count > kCand) {
+    kth_by_radix(sm, keys, n, count, k);
+    return;
   }
-  uint32_t p, q, eligible, forced;
-  scan2(sm, some, must, p, q, eligible, forced);
-  const bool all = eligible <= static_cast<uint32_t>(k);
+  const int bin = sm.bin;
+  for (int i = tid; i < n; i += kThreads)
+    if (ranked(keys[i]) && bin_of(keys[i]) == bin) sm.cand[atomicAdd(&sm.n_cand, 1u)] = keys[i];
+  __syncthreads();
+  rank_candidates(sm, k - sm.above);
+}
+
+// What the selection needs to know about a CTA's keys.
+struct Keys {
+  int n;
+  uint32_t some, must;  // eligible ones, and of them those always taken
+  float lo, hi;         // the range of the others' scores
+};
+
+// The indexes of the k largest of keys[0..n) (ties to the lower index), in
+// ascending order into sm.picked; returns how many there are.  (Not inlined:
+// the code is used in two places and fetching it is what a short call pays.)
+__device__ __noinline__ int select_k(Smem &sm, const uint64_t *keys, const Keys in, int k) {
+  const int tid = threadIdx.x, n = in.n;
+  if (n <= kDirect) {
+    bool taken = false;
+    if (tid < n) {
+      const uint64_t x = keys[tid];
+      int rank = 0;
+#pragma unroll 4
+      for (int i = 0; i < n; i++) {
+        const uint64_t y = keys[i];
+        rank += y > x || (y == x && i < tid);
+      }
+      taken = x != 0ull && rank < k;
+    }
+    const uint32_t flags = __ballot_sync(0xFFFFFFFFu, taken);
+    if ((tid & 31) == 0) sm.scan_a[tid >> 5] = __popc(flags);
+    __syncthreads();
+    int slot = __popc(flags & ((1u << (tid & 31)) - 1u)), total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+      if (w < (tid >> 5)) slot += sm.scan_a[w];
+      total += sm.scan_a[w];
+    }
+    if (taken) sm.picked[slot] = tid;
+    __syncthreads();
+    return total;
+  }
+  const bool all = in.some <= static_cast<uint32_t>(k);
   uint64_t T = 0ull;  // keys > T are taken, and `need` of those equal to it
   uint32_t need = 0;
-  if (!all && forced >= static_cast<uint32_t>(k)) {
+  if (!all && in.must >= static_cast<uint32_t>(k)) {
     T = kForced;
     need = k;
   } else if (!all) {
-    kth_largest(sm, keys, n, eligible - forced, k - forced);
+    kth_largest(sm, keys, n, in.some - in.must, k - in.must, in.lo, in.hi);
     T = sm.threshold;
     need = sm.need;
   }
@@ -250,13 +326,13 @@ __device__ int select_k(Smem &sm, const uint64_t *keys, int n, int k, Emit emit)
   uint32_t slot = pg + min(pe, need);
   for (int i = lo; i < hi; i++) {
     const uint64_t x = keys[i];
-    if (x > T || (x == T && pe < need)) emit(static_cast<int>(slot++), i);
+    if (x > T || (x == T && pe < need)) sm.picked[slot++] = i;
     pe += x == T;
   }
-  return static_cast<int>(all ? eligible : static_cast<uint32_t>(k));
+  __syncthreads();
+  return static_cast<int>(all ? in.some : static_cast<uint32_t>(k));
 }
 
-// gridDim.x = G * B * T: CTA r of row bt's cluster is block bt * G + r
 __global__ void __launch_bounds__(kThreads) block_select_kernel(const lidx_block_select_args a, int G, int shift,
                                                                  int slice_cap, uint32_t *status) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -272,25 +348,69 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const lidx_block
   pdl_trigger();
   pdl_wait();
 
-  // ---- the row's queries in 8 bits: thread (head, quarter) owns 32 dims
+  // ---- this CTA's blocks [j0, j1) of the nb that the query sees; the first ones' codes are fetched
+  // while the queries are rounded
+  const int g = lane >> 2, c = lane & 3;
+  const int64_t most = static_cast<int64_t>(a.max_pages) << shift;
+  const int32_t len_in = __ldg(a.len + b);
+  const int qh = tid >> 2, qc = tid & 3;  // queries: thread (head, quarter) owns 32 dims
+  uint4 qw[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    qw[i] = make_uint4(0, 0, 0, 0);
+    if (qh < a.H)
+      qw[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + (bt * a.H + qh) * 128 + 32 * qc) + i);
+  }
+  const float qweight = qh < a.H ? __ldg(a.w + bt * a.H + qh) : 0.f;
+  if (len_in > most && rank == 0 && tid == 0) raise_status(status, LIDX_DEV_BOUNDS);
+  const int64_t seen = min(static_cast<int64_t>(max(len_in, 0)), most) - (a.T - 1 - t);
+  const int nb = seen > 0 ? static_cast<int>((seen + a.page_rows - 1) >> shift) : 0;
+  const int per = ((nb + G - 1) / G + 7) & ~7;
+  const int j0 = min(rank * per, nb), j1 = min(j0 + per, nb);
+  const int32_t *table = a.table + static_cast<int64_t>(b) * a.ld_table;
+  bool no_page = false, not_a_number = false;
+  auto page_at = [&](int j) {  // of block j, -1 where there is none
+    if (j >= j1) return -1;
+    const int32_t p = __ldg(table + j);
+    return p;
+  };
+  struct Codes {
+    uint4 x, y;  // bytes [32 c, 32 c + 32)
+    float scale;
+    int32_t page;
+  };
+  auto codes_of = [&](int32_t p, bool exists) {
+    Codes k;
+    k.x = k.y = make_uint4(0, 0, 0, 0);
+    k.scale = 0.f;
+    k.page = p < 0 || p >= a.n_pages ? -1 : p;
+    no_page |= exists && k.page < 0;
+    if (k.page >= 0) {
+      const uint4 *src = reinterpret_cast<const uint4 *>(a.codes + static_cast<int64_t>(k.page) * 128 + 32 * c);
+      k.x = __ldg(src);
+      k.y = __ldg(src + 1);
+      k.scale = __ldg(a.scale + k.page);
+    }
+    return k;
+  };
+  // blocks j + g (lane (g, c)) of the steps j = j0 + 8 warp, + 8 kWarps, ..: two pages and one step's codes ahead
+  const int first = j0 + 8 * warp + g;
+  int32_t page1 = page_at(first);
+  Codes now = codes_of(page1, first < j1);
+  page1 = page_at(first + 8 * kWarps);
+
+  // ---- the row's queries in 8 bits
   {
-    const int h = tid >> 2, c = tid & 3;
+    const int h = qh, c = qc;
     float v[32], top = 0.f;
-    if (h < a.H) {
-      const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + (bt * a.H + h) * 128 + 32 * c);
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const uint4 w = __ldg(src + i);
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    for (int i = 0; i < 4; i++) {
+      const uint32_t x[4] = {qw[i].x, qw[i].y, qw[i].z, qw[i].w};
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
-          v[8 * i + 2 * k] = bf16x2_lo(x[k]);
-          v[8 * i + 2 * k + 1] = bf16x2_hi(x[k]);
-        }
+      for (int k = 0; k < 4; k++) {
+        v[8 * i + 2 * k] = bf16x2_lo(x[k]);
+        v[8 * i + 2 * k + 1] = bf16x2_hi(x[k]);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; i++) v[i] = 0.f;
     }
     bool nan = false;
 #pragma unroll
@@ -317,10 +437,9 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const lidx_block
     dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
     dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
     if (c == 0)
-      sm.weight[h] = h < a.H ? static_cast<double>(__fmul_rn(__ldg(a.w + bt * a.H + h), __fmul_rn(top, 1.f / 127.f))) : 0.;
+      sm.weight[h] = h < a.H ? static_cast<double>(__fmul_rn(qweight, __fmul_rn(top, 1.f / 127.f))) : 0.;
   }
   __syncthreads();
-  const int g = lane >> 2, c = lane & 3;
   uint32_t A[4][4][4];  // [tile][step][register]
   double weight[8];
 #pragma unroll
@@ -338,33 +457,16 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const lidx_block
     }
   }
 
-  // ---- this CTA's blocks [j0, j1) of the nb that the query sees
-  const int64_t most = static_cast<int64_t>(a.max_pages) << shift;
-  const int32_t len_in = __ldg(a.len + b);
-  if (len_in > most && rank == 0 && tid == 0) raise_status(status, LIDX_DEV_BOUNDS);
-  const int64_t seen = min(static_cast<int64_t>(max(len_in, 0)), most) - (a.T - 1 - t);
-  const int nb = seen > 0 ? static_cast<int>((seen + a.page_rows - 1) >> shift) : 0;
-  const int per = ((nb + G - 1) / G + 7) & ~7;
-  const int j0 = min(rank * per, nb), j1 = min(j0 + per, nb);
-  const int32_t *table = a.table + static_cast<int64_t>(b) * a.ld_table;
-  bool no_page = false, not_a_number = false;
+  // ---- scores
   const int heads_tiles = (a.H + 15) / 16;
+  float lo = INFINITY, hi = -INFINITY;
+  uint32_t some = 0, must = 0;
+#pragma unroll 1
   for (int j = j0 + 8 * warp; j < j1; j += 8 * kWarps) {
-    // lane (g, c) loads bytes [32 c, 32 c + 32) of block j + g
-    const int jb = j + g;
-    int32_t page = jb < j1 ? __ldg(table + jb) : -1;
-    if (page < 0 || page >= a.n_pages) {
-      no_page |= jb < j1;
-      page = -1;
-    }
-    uint4 x = make_uint4(0, 0, 0, 0), y = x;
-    float scale = 0.f;
-    if (page >= 0) {
-      const uint4 *src = reinterpret_cast<const uint4 *>(a.codes + static_cast<int64_t>(page) * 128 + 32 * c);
-      x = __ldg(src);
-      y = __ldg(src + 1);
-      scale = __ldg(a.scale + page);
-    }
+    const Codes k = now;
+    now = codes_of(page1, j + 8 * kWarps + g < j1);
+    page1 = page_at(j + 16 * kWarps + g);
+    const uint4 x = k.x, y = k.y;
     // lane (g, c) ends with heads g, g + 8 of each tile for blocks j + 2c, j + 2c + 1
     double s0 = 0., s1 = 0.;
 #pragma unroll
@@ -388,32 +490,61 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const lidx_block
     }
     // lane (g, 0..3) < 8: block j + lane; its sum sits in s0 / s1 of lane c = lane / 2, its scale and page in lane 4 * lane
     const double sa = __shfl_sync(0xFFFFFFFFu, s0, (lane & 7) >> 1), sb = __shfl_sync(0xFFFFFFFFu, s1, (lane & 7) >> 1);
-    const float sc = __shfl_sync(0xFFFFFFFFu, scale, 4 * (lane & 7));
-    const int32_t pg = __shfl_sync(0xFFFFFFFFu, page, 4 * (lane & 7));
+    const float sc = __shfl_sync(0xFFFFFFFFu, k.scale, 4 * (lane & 7));
+    const int32_t pg = __shfl_sync(0xFFFFFFFFu, k.page, 4 * (lane & 7));
     const int jl = j + lane;
     if (lane < 8 && jl < j1) {
       const double score = ((lane & 1) ? sb : sa) * static_cast<double>(sc);
       uint64_t key = pg >= 0 ? key_of(score) : 0ull;
-      if (jl < a.n_first || jl >= nb - a.n_last) key = kForced;
-      else if (pg >= 0 && key == 0ull) not_a_number = true;
+      if (jl < a.n_first || jl >= nb - a.n_last) {
+        key = kForced;
+        must++;
+      } else if (key) {
+        lo = fminf(lo, static_cast<float>(score));
+        hi = fmaxf(hi, static_cast<float>(score));
+      } else if (pg >= 0) {
+        not_a_number = true;
+      }
+      some += key != 0ull;
       keys[jl - j0] = key;
     }
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {  // lanes 0-7
+    lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+    some += __shfl_xor_sync(0xFFFFFFFFu, some, o);
+    must += __shfl_xor_sync(0xFFFFFFFFu, must, o);
+  }
+  if (lane == 0) {
+    sm.red_lo[warp] = lo;
+    sm.red_hi[warp] = hi;
+    sm.red_some[warp] = some;
+    sm.red_must[warp] = must;
   }
   if (no_page) raise_status(status, LIDX_DEV_BOUNDS);
   if (not_a_number) raise_status(status, LIDX_DEV_NAN);
   __syncthreads();
+  Keys mine_in = {j1 - j0, 0u, 0u, INFINITY, -INFINITY};
+#pragma unroll
+  for (int w = 0; w < kWarps; w++) {
+    mine_in.some += sm.red_some[w];
+    mine_in.must += sm.red_must[w];
+    mine_in.lo = fminf(mine_in.lo, sm.red_lo[w]);
+    mine_in.hi = fmaxf(mine_in.hi, sm.red_hi[w]);
+  }
 
   int32_t *ids = a.ids + bt * a.k;
-  int n_sel;
-  if (G == 1) {
-    n_sel = select_k(sm, keys, j1 - j0, a.k, [&](int slot, int i) { ids[slot] = i; });
-  } else {
+  int n_sel = select_k(sm, keys, mine_in, a.k);
+  int32_t id = tid < n_sel ? j0 + sm.picked[tid] : -1;  // kMaxK <= kThreads
+  if (G > 1) {
     cluster_wait();  // the first CTA runs: its shared memory may be written
-    const uint32_t to_key = remote(in_key + rank * a.k, 0), to_id = remote(in_id + rank * a.k, 0);
-    const int mine = select_k(sm, keys, j1 - j0, a.k, [&](int slot, int i) {
-      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to_key + 8 * slot), "l"(keys[i]) : "memory");
-      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to_id + 4 * slot), "r"(j0 + i) : "memory");
-    });
+    const int mine = n_sel;
+    if (tid < mine) {
+      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote(in_key + rank * a.k + tid, 0)), "l"(keys[id - j0])
+                   : "memory");
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote(in_id + rank * a.k + tid, 0)), "r"(id) : "memory");
+    }
     if (tid == 0)
       asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote(&sm.in_count[rank], 0)), "r"(mine) : "memory");
     __syncthreads();
@@ -425,31 +556,65 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const lidx_block
     for (int r = 1; r < G; r++) {
       const int cnt = sm.in_count[r];
       uint64_t key = 0;
-      int32_t id = 0;
+      int32_t one = 0;
       if (tid < cnt) {
         key = in_key[r * a.k + tid];
-        id = in_id[r * a.k + tid];
+        one = in_id[r * a.k + tid];
       }
       __syncthreads();
       if (tid < cnt) {
         in_key[n + tid] = key;
-        in_id[n + tid] = id;
+        in_id[n + tid] = one;
       }
       n += cnt;
     }
+    // (every entry is eligible; the range of their scores, from the lists)
+    Keys all_in = {n, static_cast<uint32_t>(n), 0u, INFINITY, -INFINITY};
     __syncthreads();
-    n_sel = select_k(sm, in_key, n, a.k, [&](int slot, int i) { ids[slot] = in_id[i]; });
+    if (n > kDirect) {
+      lo = INFINITY;
+      hi = -INFINITY;
+      must = 0;
+      for (int i = tid; i < n; i += kThreads) {
+        if (ranked(in_key[i])) {
+          lo = fminf(lo, value_of(in_key[i]));
+          hi = fmaxf(hi, value_of(in_key[i]));
+        } else {
+          must++;
+        }
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+        must += __shfl_xor_sync(0xFFFFFFFFu, must, o);
+      }
+      if (lane == 0) {
+        sm.red_lo[warp] = lo;
+        sm.red_hi[warp] = hi;
+        sm.red_must[warp] = must;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kWarps; w++) {
+        all_in.must += sm.red_must[w];
+        all_in.lo = fminf(all_in.lo, sm.red_lo[w]);
+        all_in.hi = fmaxf(all_in.hi, sm.red_hi[w]);
+      }
+    }
+    n_sel = select_k(sm, in_key, all_in, a.k);
+    id = tid < n_sel ? in_id[sm.picked[tid]] : -1;
   }
-  for (int i = n_sel + tid; i < a.k; i += kThreads) ids[i] = -1;
+  if (tid < a.k) ids[tid] = id;
   if (tid == 0 && a.n_sel) a.n_sel[bt] = n_sel;
 }
 
 // CTAs a row is split over: so that a slice fits, and, while the rows leave
-// SMs idle, down to 256 blocks a CTA.
+// SMs idle, down to 128 blocks a CTA.
 int cluster_for(const lidx_block_select_args &a) {
   int g = 1;
   while (g < kMaxCluster && (a.max_pages > g * kMaxSlice ||
-                             (a.max_pages > g * 256 && static_cast<int64_t>(a.B) * a.T * g * 2 <= 2 * 148)))
+                             (a.max_pages > g * 128 && static_cast<int64_t>(a.B) * a.T * g * 2 <= 148)))
     g *= 2;
   return g;
 }

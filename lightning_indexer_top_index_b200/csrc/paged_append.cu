@@ -45,136 +45,121 @@ __device__ __forceinline__ void load16(const void *x, int dtype, int64_t at, flo
   }
 }
 
-// kPer rows a group of lanes, all loads of which are in flight together.
-template <int kDim, int kPer>
+template <int kDim>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const lidx_paged_append_args a, int shift,
                                                                  uint32_t *status) {
   constexpr int kLanes = kDim / 16;          // lanes of a row
   constexpr int kAngles = 32 / kLanes;       // angles a lane evaluates
   const int t = threadIdx.x % kLanes, lane = threadIdx.x & 31;
   const int base = lane - t;                 // the row's first lane
-  const int64_t i0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / kLanes) + threadIdx.x / kLanes) * kPer;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / kLanes) + threadIdx.x / kLanes;
   const int rl = t - (kLanes - 4);  // >= 0: lane rl of the four that hold the 64 RoPE dims
   float freq[kAngles];
   pdl_trigger();
   pdl_wait();  // rows, positions and tables may come from the previous kernel
   // lanes of rows behind the last one stay for the shuffles
-  int seq[kPer], row[kPer], pos[kPer];
-  int32_t dst[kPer];
-  float v[kPer][16];
+  int seq = -1, row = -1, pos = 0;
+  float x[16];
 #pragma unroll
-  for (int r = 0; r < kPer; r++) {
-    const int64_t i = i0 + r;
-    seq[r] = row[r] = -1;
-    pos[r] = 0;
-#pragma unroll
-    for (int k = 0; k < 16; k++) v[r][k] = 0.f;
-    if (i < a.n) {
-      seq[r] = __ldg(a.seq + i);
-      row[r] = __ldg(a.row + i);
-      if (a.inv_freq) pos[r] = a.pos ? __ldg(a.pos + i) : row[r];
-      load16(a.x, a.x_dtype, i * a.ld_x + 16 * t, v[r]);
-    }
+  for (int k = 0; k < 16; k++) x[k] = 0.f;
+  if (i < a.n) {
+    seq = __ldg(a.seq + i);
+    row = __ldg(a.row + i);
+    if (a.inv_freq) pos = a.pos ? __ldg(a.pos + i) : row;
+    load16(a.x, a.x_dtype, i * a.ld_x + 16 * t, x);
   }
   if (a.inv_freq) {
 #pragma unroll
     for (int k = 0; k < kAngles; k++) freq[k] = __ldg(a.inv_freq + t * kAngles + k);
   }
+  int32_t dst = -1;
+  if (seq >= 0) {
+    if (seq < a.B && row >= 0) dst = pool_row(a.cache, shift, seq, row);
+    if (dst < 0 && t == 0) raise_status(status, LIDX_DEV_BOUNDS);
+  }
+  // the largest magnitude by its bits; infinities and NaNs have the largest
+  uint32_t top = 0u;
 #pragma unroll
-  for (int r = 0; r < kPer; r++) {
-    dst[r] = -1;
-    if (seq[r] >= 0) {
-      if (seq[r] < a.B && row[r] >= 0) dst[r] = pool_row(a.cache, shift, seq[r], row[r]);
-      if (dst[r] < 0 && t == 0) raise_status(status, LIDX_DEV_BOUNDS);
+  for (int k = 0; k < 16; k++) top = max(top, __float_as_uint(x[k]) & 0x7FFFFFFFu);
+  const bool nonfinite = top >= 0x7F800000u;
+  if (nonfinite && dst >= 0) raise_status(status, LIDX_DEV_NAN);
+  const bool odd = __any_sync(kAll, nonfinite);  // the warp's rows take the careful way
+  if (odd) {
+    top = 0u;
+#pragma unroll
+    for (int k = 0; k < 16; k++) top = isfinite(x[k]) ? max(top, __float_as_uint(x[k]) & 0x7FFFFFFFu) : top;
+  }
+  // ... of the block: two or four neighbouring lanes
+  const int dtype = a.cache.rows.dtype;
+  top = max(top, __shfl_xor_sync(kAll, top, 1));
+  if (dtype == LIDX_E4M3) top = max(top, __shfl_xor_sync(kAll, top, 2));
+
+  if (a.inv_freq) {
+    float cs[kAngles], sn[kAngles];
+#pragma unroll
+    for (int k = 0; k < kAngles; k++) {
+      double turns = static_cast<double>(pos) * static_cast<double>(freq[k]) * 0.15915494309189533577;
+      turns -= rint(turns);
+      sincospif(2.f * static_cast<float>(turns), &sn[k], &cs[k]);
+    }
+    const int from = rl < 0 ? 0 : rl;
+    if (a.rope_pairs == LIDX_ROPE_ADJACENT) {  // lane rl holds pairs 8 rl .. 8 rl + 7
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        // pair 8 rl + k: angle slot (8 rl + k) % kAngles of lane (8 rl + k) / kAngles
+        const int src = base + (8 * from + k) / kAngles;
+        const float c = __shfl_sync(kAll, cs[k % kAngles], src), s = __shfl_sync(kAll, sn[k % kAngles], src);
+        if (rl >= 0) {
+          const float p = x[2 * k], q = x[2 * k + 1];
+          x[2 * k] = fmaf(p, c, -(q * s));
+          x[2 * k + 1] = fmaf(p, s, q * c);
+        }
+      }
+    } else {  // lanes 0, 1 hold the first halves of the pairs 16 (rl & 1) .. + 15, lanes 2, 3 their second halves
+#pragma unroll
+      for (int k = 0; k < 16; k++) {
+        const int src = base + (16 * (from & 1) + k) / kAngles;
+        const float c = __shfl_sync(kAll, cs[k % kAngles], src);
+        const float s = __shfl_sync(kAll, sn[k % kAngles], src);
+        const float o = __shfl_xor_sync(kAll, x[k], 2);
+        if (rl >= 0) x[k] = rl < 2 ? fmaf(x[k], c, -(o * s)) : fmaf(o, s, x[k] * c);
+      }
     }
   }
-#pragma unroll
-  for (int r = 0; r < kPer; r++) {
-    float(&x)[16] = v[r];
-    // the largest magnitude by its bits; infinities and NaNs have the largest
-    uint32_t top = 0u;
-#pragma unroll
-    for (int k = 0; k < 16; k++) top = max(top, __float_as_uint(x[k]) & 0x7FFFFFFFu);
-    const bool nonfinite = top >= 0x7F800000u;
-    if (nonfinite && dst[r] >= 0) raise_status(status, LIDX_DEV_NAN);
-    const bool odd = __any_sync(kAll, nonfinite);  // the warp's rows take the careful way
-    if (odd) {
-      top = 0u;
-#pragma unroll
-      for (int k = 0; k < 16; k++) top = isfinite(x[k]) ? max(top, __float_as_uint(x[k]) & 0x7FFFFFFFu) : top;
-    }
-    // ... of the block: two or four neighbouring lanes
-    const int dtype = a.cache.rows.dtype;
-    top = max(top, __shfl_xor_sync(kAll, top, 1));
-    if (dtype == LIDX_E4M3) top = max(top, __shfl_xor_sync(kAll, top, 2));
 
-    if (a.inv_freq) {
-      float cs[kAngles], sn[kAngles];
-#pragma unroll
-      for (int k = 0; k < kAngles; k++) {
-        double turns = static_cast<double>(pos[r]) * static_cast<double>(freq[k]) * 0.15915494309189533577;
-        turns -= rint(turns);
-        sincospif(2.f * static_cast<float>(turns), &sn[k], &cs[k]);
-      }
-      const int from = rl < 0 ? 0 : rl;
-      if (a.rope_pairs == LIDX_ROPE_ADJACENT) {  // lane rl holds pairs 8 rl .. 8 rl + 7
-#pragma unroll
-        for (int k = 0; k < 8; k++) {
-          // pair 8 rl + k: angle slot (8 rl + k) % kAngles of lane (8 rl + k) / kAngles
-          const int src = base + (8 * from + k) / kAngles;
-          const float c = __shfl_sync(kAll, cs[k % kAngles], src), s = __shfl_sync(kAll, sn[k % kAngles], src);
-          if (rl >= 0) {
-            const float p = x[2 * k], q = x[2 * k + 1];
-            x[2 * k] = fmaf(p, c, -(q * s));
-            x[2 * k + 1] = fmaf(p, s, q * c);
-          }
-        }
-      } else {  // lanes 0, 1 hold the first halves of the pairs 16 (rl & 1) .. + 15, lanes 2, 3 their second halves
-#pragma unroll
-        for (int k = 0; k < 16; k++) {
-          const int src = base + (16 * (from & 1) + k) / kAngles;
-          const float c = __shfl_sync(kAll, cs[k % kAngles], src);
-          const float s = __shfl_sync(kAll, sn[k % kAngles], src);
-          const float o = __shfl_xor_sync(kAll, x[k], 2);
-          if (rl >= 0) x[k] = rl < 2 ? fmaf(x[k], c, -(o * s)) : fmaf(o, s, x[k] * c);
-        }
-      }
-    }
+  if (dst < 0) return;
 
-    if (dst[r] < 0) continue;
-
-    const lidx_kv &kv = a.cache.rows;
-    const int64_t p = dst[r];
-    if (dtype == LIDX_F32) {
-      float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(const_cast<void *>(kv.data)) + p * kv.ld + 16 * t);
+  const lidx_kv &kv = a.cache.rows;
+  const int64_t p = dst;
+  if (dtype == LIDX_F32) {
+    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(const_cast<void *>(kv.data)) + p * kv.ld + 16 * t);
 #pragma unroll
-      for (int k = 0; k < 4; k++) o[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-    } else if (dtype == LIDX_BF16 || rl >= 0) {
-      uint16_t *o = dtype == LIDX_BF16 ? static_cast<uint16_t *>(const_cast<void *>(kv.data)) + p * kv.ld + 16 * t
-                                       : static_cast<uint16_t *>(const_cast<void *>(kv.rope)) + p * kv.ld_rope + 16 * rl;
-      reinterpret_cast<uint4 *>(o)[0] = pack8_bf16(x);
-      reinterpret_cast<uint4 *>(o)[1] = pack8_bf16(x + 8);
+    for (int k = 0; k < 4; k++) o[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+  } else if (dtype == LIDX_BF16 || rl >= 0) {
+    uint16_t *o = dtype == LIDX_BF16 ? static_cast<uint16_t *>(const_cast<void *>(kv.data)) + p * kv.ld + 16 * t
+                                     : static_cast<uint16_t *>(const_cast<void *>(kv.rope)) + p * kv.ld_rope + 16 * rl;
+    reinterpret_cast<uint4 *>(o)[0] = odd ? pack8_bf16(x) : pack8_bf16_numbers(x);
+    reinterpret_cast<uint4 *>(o)[1] = odd ? pack8_bf16(x + 8) : pack8_bf16_numbers(x + 8);
+  } else {
+    const bool e4m3 = dtype == LIDX_E4M3;
+    const float am = __uint_as_float(top);
+    const int e = top ? (e4m3 ? block_exponent_e4m3(am) : block_exponent_e2m1(am)) : 0;
+    const float inv = inverse_scale(e);
+#pragma unroll
+    for (int k = 0; k < 16; k++) x[k] *= inv;
+    uint8_t *data = static_cast<uint8_t *>(const_cast<void *>(kv.data)) + p * kv.ld;
+    uint8_t *scale = const_cast<uint8_t *>(kv.scale) + p * kv.ld_scale;
+    if (e4m3) {
+      *reinterpret_cast<uint4 *>(data + 16 * t) =
+          odd ? make_uint4(pack4_e4m3(x), pack4_e4m3(x + 4), pack4_e4m3(x + 8), pack4_e4m3(x + 12))
+              : make_uint4(pack4_e4m3_in_range(x), pack4_e4m3_in_range(x + 4), pack4_e4m3_in_range(x + 8),
+                           pack4_e4m3_in_range(x + 12));
+      if ((t & 3) == 0) scale[t / 4] = static_cast<uint8_t>(e + 127);
     } else {
-      const bool e4m3 = dtype == LIDX_E4M3;
-      const float am = __uint_as_float(top);
-      const int e = top ? (e4m3 ? block_exponent_e4m3(am) : block_exponent_e2m1(am)) : 0;
-      const float inv = inverse_scale(e);
-#pragma unroll
-      for (int k = 0; k < 16; k++) x[k] *= inv;
-      uint8_t *data = static_cast<uint8_t *>(const_cast<void *>(kv.data)) + p * kv.ld;
-      uint8_t *scale = const_cast<uint8_t *>(kv.scale) + p * kv.ld_scale;
-      if (e4m3) {
-        *reinterpret_cast<uint4 *>(data + 16 * t) =
-            odd ? make_uint4(pack4_e4m3(x), pack4_e4m3(x + 4), pack4_e4m3(x + 8), pack4_e4m3(x + 12))
-                : make_uint4(pack4_e4m3_in_range(x), pack4_e4m3_in_range(x + 4), pack4_e4m3_in_range(x + 8),
-                             pack4_e4m3_in_range(x + 12));
-        if ((t & 3) == 0) scale[t / 4] = static_cast<uint8_t>(e + 127);
-      } else {
-        *reinterpret_cast<uint2 *>(data + 8 * t) = 
-            odd ? make_uint2(pack8_e2m1(x), pack8_e2m1(x + 8))
-                : make_uint2(pack8_e2m1_finite(x), pack8_e2m1_finite(x + 8));
-        if ((t & 1) == 0) scale[t / 2] = static_cast<uint8_t>(e + 127);
-      }
+      *reinterpret_cast<uint2 *>(data + 8 * t) = 
+          odd ? make_uint2(pack8_e2m1(x), pack8_e2m1(x + 8))
+              : make_uint2(pack8_e2m1_finite(x), pack8_e2m1_finite(x + 8));
+      if ((t & 1) == 0) scale[t / 2] = static_cast<uint8_t>(e + 127);
     }
   }
 }
@@ -229,19 +214,16 @@ unsigned blocks(int64_t n, int lanes, int per) {
 
 int page_shift(const lidx_pages &c) { return __builtin_ctz(static_cast<unsigned>(c.page_rows)); }
 
-// Few rows are spread as thin as they go, many go several a thread (from
-// kManyThreads threads' worth on, about a full machine): at 20011 rows of 512
-// fp32 values PLACEHOLDER_A.
-constexpr int64_t kManyThreads = 148 * 2048;
-
 cudaError_t launch_paged_append(const lidx_paged_append_args &a, void *ws, cudaStream_t st) {
-  const int lanes = a.cache.rows.dim / 16;
-  const bool many = static_cast<int64_t>(a.n) * lanes >= kManyThreads;
-  auto kern = a.cache.rows.dim == 512 ? (many ? paged_append_kernel<512, 2> : paged_append_kernel<512, 1>)
-                                      : (many ? paged_append_kernel<128, 2> : paged_append_kernel<128, 1>);
-  return launch_kernel(kern, dim3(blocks(a.n, lanes, many ? 2 : 1)), dim3(kThreads), 0, st,
+  auto kern = a.cache.rows.dim == 512 ? paged_append_kernel<512> : paged_append_kernel<128>;
+  return launch_kernel(kern, dim3(blocks(a.n, a.cache.rows.dim / 16, 1)), dim3(kThreads), 0, st,
                        (a.flags & LIDX_LAUNCH_PDL) != 0, a, page_shift(a.cache), static_cast<uint32_t *>(ws));
 }
+
+// Few rows are read one a thread; from about a machine full of threads on,
+// four (20011 rows of 512 in 4 bits: 13.1 us against 17.0 with one; 64 rows
+// 4.0 us with one).
+constexpr int64_t kManyThreads = 148 * 2048;
 
 cudaError_t launch_paged_read(const lidx_paged_read_args &a, void *ws, cudaStream_t st) {
   const int lanes = a.cache.rows.dim / 8;

@@ -82,6 +82,17 @@ __device__ __forceinline__ uint32_t bf16_bits(float x) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(x));
 }
 
+// pack8_bf16 of values that are not NaN
+__device__ __forceinline__ uint4 pack8_bf16_numbers(const float *v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const __nv_bfloat162 two = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&two);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 __device__ __forceinline__ uint4 pack8_bf16(const float *v) {
   uint32_t w[4];
 #pragma unroll
