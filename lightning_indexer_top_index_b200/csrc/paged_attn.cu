@@ -31,9 +31,11 @@
 //     TMEM: at 8 one of the 64 heads made most chunks pay for it.  Sums are of
 //     the fp32 probabilities; floating point loses nothing by a common factor
 //     up to 2^32.
-//   P is rounded to bf16 for the second product: 2^-9 of each probability,
-//   independent errors that average out to less than the bf16 output's own
-//   rounding.
+//   P is rounded to bf16 for the second product, 2^-9 of each probability.  O
+//   is divided by the sum of the rounded ones, so that its weights add up to
+//   one and a row that has nearly all of it comes out exactly (by the unrounded
+//   sum the error over peaked rows was 1.6 times that of an exact P); lse takes
+//   the unrounded sum.
 //
 // The loops are kept small (one place each for a product, a load, a store):
 // unrolled over their chunks they outgrew the instruction cache, and the
@@ -93,7 +95,7 @@ struct __align__(16) Smem {
   uint32_t tmem_base;
   uint32_t abort;
   float alpha[2][kH];             // rescale factors of a chunk
-  float l[kH];
+  float l[kH];                    // 1 / sum of the rounded probabilities
   // the CTA's first chunk
   int32_t job, chunk;
   int32_t scan[kThreads / 32];
@@ -111,7 +113,7 @@ struct __align__(16) Split {
 struct Scratch {
   uint32_t *status;
   Split *split;  // [G]
-  float2 *ml;    // [2 * G][kH]
+  float4 *ml;    // [2 * G][kH]: maximum, sum, sum of the rounded probabilities
   float4 *o;     // [2 * G][kH / 4][kD], four heads together: as TMEM holds them
 };
 
@@ -618,9 +620,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (cut && tid == 0) raise_status(ws.status, LIDX_DEV_BOUNDS);
     }
     const int h0 = warp * 16 + (lane >> 2), h1 = h0 + 8;  // this lane's heads
-    const float c2 = a.scale * kLog2e;
+    // logits are s * c2 in base 2; with a negative scale s changes sign instead, and a zero one
+    // becomes one that makes every product round away (0 * -inf would be NaN)
+    const bool negative = a.scale < 0.f;
+    const float c2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
     const uint32_t quarter = static_cast<uint32_t>(warp * 32) << 16;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, r0 = 0.f, r1 = 0.f;  // r: of the rounded probabilities
     bool first_segment = true;  // the CTA's first job
     // After a wait that gave up the warp goes through the rest of its chunks
     // without touching TMEM or global memory, for the others' barriers.
@@ -660,12 +665,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm->s_free);
       float t0 = -INFINITY, t1 = -INFINITY;
+      if (negative || (v0 & v1) != 0xFFFFFFFFu) {
 #pragma unroll
-      for (int u = 0; u < 16; u++) {  // row 8 (u / 2) + 2 (lane % 4) + u % 2
-        const uint32_t bits = (u < 8 ? v0 : v1) >> (2 * (lane & 3));
-        const bool in = (bits >> (8 * ((u >> 1) & 3) + (u & 1))) & 1u;
-        s0[u] = in ? s0[u] * c2 : -INFINITY;
-        s1[u] = in ? s1[u] * c2 : -INFINITY;
+        for (int u = 0; u < 16; u++) {  // row 8 (u / 2) + 2 (lane % 4) + u % 2
+          const uint32_t bits = (u < 8 ? v0 : v1) >> (2 * (lane & 3));
+          const bool in = (bits >> (8 * ((u >> 1) & 3) + (u & 1))) & 1u;
+          s0[u] = in ? (negative ? -s0[u] : s0[u]) : -INFINITY;
+          s1[u] = in ? (negative ? -s1[u] : s1[u]) : -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 16; u++) {
         t0 = fmaxf(t0, s0[u]);
         t1 = fmaxf(t1, s1[u]);
       }
@@ -674,6 +684,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         t0 = fmaxf(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, o));
         t1 = fmaxf(t1, __shfl_xor_sync(0xFFFFFFFFu, t1, o));
       }
+      t0 *= c2;
+      t1 *= c2;
       // the reference maximum moves only on rises above kLazy (the first rise
       // from -inf finds an O of zeros: nothing to rescale)
       const float n0 = t0 <= m0 + kLazy ? m0 : fmaxf(t0, m0), n1 = t1 <= m1 + kLazy ? m1 : fmaxf(t1, m1);
@@ -683,6 +695,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       m1 = n1;
       l0 *= a0;
       l1 *= a1;
+      r0 *= a0;
+      r1 *= a1;
       const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
       if ((lane & 3) == 0) {
         sm->alpha[stage][h0] = a0;
@@ -708,13 +722,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint8_t *p0 = sP + stage * kPBytes + h0 * 128 + 4 * (lane & 3), *p1 = p0 + 8 * 128;
 #pragma unroll
       for (int u = 0; u < 8; u++) {
-        const float x0 = exp2_approx(s0[2 * u] - b0), x1 = exp2_approx(s0[2 * u + 1] - b0);
-        const float y0 = exp2_approx(s1[2 * u] - b1), y1 = exp2_approx(s1[2 * u + 1] - b1);
+        const float x0 = exp2_approx(fmaf(s0[2 * u], c2, -b0)), x1 = exp2_approx(fmaf(s0[2 * u + 1], c2, -b0));
+        const float y0 = exp2_approx(fmaf(s1[2 * u], c2, -b1)), y1 = exp2_approx(fmaf(s1[2 * u + 1], c2, -b1));
         l0 += x0 + x1;
         l1 += y0 + y1;
         const __nv_bfloat162 px = __floats2bfloat162_rn(x0, x1), py = __floats2bfloat162_rn(y0, y1);
-        *reinterpret_cast<uint32_t *>(p0 + ((u ^ (h0 & 7)) << 4)) = *reinterpret_cast<const uint32_t *>(&px);
-        *reinterpret_cast<uint32_t *>(p1 + ((u ^ (h0 & 7)) << 4)) = *reinterpret_cast<const uint32_t *>(&py);
+        const uint32_t wx = *reinterpret_cast<const uint32_t *>(&px), wy = *reinterpret_cast<const uint32_t *>(&py);
+        r0 += bf16x2_lo(wx) + bf16x2_hi(wx);
+        r1 += bf16x2_lo(wy) + bf16x2_hi(wy);
+        *reinterpret_cast<uint32_t *>(p0 + ((u ^ (h0 & 7)) << 4)) = wx;
+        *reinterpret_cast<uint32_t *>(p1 + ((u ^ (h0 & 7)) << 4)) = wy;
       }
       tc::fence_proxy_async_smem();
       tc::tc_fence_before();
@@ -730,18 +747,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int o = 1; o < 4; o <<= 1) {
           l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, o);
           l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, o);
+          r0 += __shfl_xor_sync(0xFFFFFFFFu, r0, o);
+          r1 += __shfl_xor_sync(0xFFFFFFFFu, r1, o);
         }
         const int heads = min(kH, a.H - g * kH);
         const int64_t out_row = static_cast<int64_t>(bt) * a.H + g * kH;
         const int64_t slot_o = 2 * static_cast<int64_t>(blockIdx.x) + (first_segment ? 0 : 1);
         if ((lane & 3) < 2 && ok) {
           const int h = (lane & 1) ? h1 : h0;
-          const float m = (lane & 1) ? m1 : m0, l = (lane & 1) ? l1 : l0;
+          const float m = (lane & 1) ? m1 : m0, l = (lane & 1) ? l1 : l0, rounded = (lane & 1) ? r1 : r0;
           if (out_now) {
-            sm->l[h] = l == 0.f ? 0.f : 1.f / l;
+            sm->l[h] = rounded == 0.f ? 0.f : 1.f / rounded;
             if (a.lse && h < heads) a.lse[out_row + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
           } else {
-            ws.ml[slot_o * kH + h] = make_float2(m, l);
+            ws.ml[slot_o * kH + h] = make_float4(m, l, rounded, 0.f);
           }
         }
         bar_or(1, 32 * kSoftmaxWarps, 0u);  // sm->l is in
@@ -791,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm->o_free);
         m0 = m1 = -INFINITY;
-        l0 = l1 = 0.f;
+        l0 = l1 = r0 = r1 = 0.f;
         first_segment = false;
       }
     }
@@ -819,7 +838,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const l
   constexpr int kWarps = kMergeThreads / 32, kItems = (kH / 4) * (kD / 32);
   __shared__ Split list[kMaxCtas];  // jobs with few partials from the front, with many from the back
   __shared__ int32_t count[2][kWarps];
-  __shared__ float4 weight_s[kMaxCtas], acc_s[kWarps][32], red_s[2][kWarps];
+  __shared__ float4 weight_s[kMaxCtas], acc_s[kWarps][32], red_s[3][kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   pdl_wait();  // the partial results come from the previous kernel
@@ -848,26 +867,23 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const l
   if (sp.job >= 0) list[many ? kMaxCtas - 1 - at : at] = sp;
   __syncthreads();
 
-  float m[4], l[4], e[4];  // of four heads of the partial that the thread looks after
-  auto look = [&](const float2 *ml) {
+  float m[4], l[4], r[4], e[4];  // of four heads of the partial that the thread looks after
+  auto look = [&](const float4 *ml) {
 #pragma unroll
     for (int k = 0; k < 4; k++) {
-      m[k] = -INFINITY;
-      l[k] = 0.f;
-    }
-    if (ml) {
-      const float4 x = reinterpret_cast<const float4 *>(ml)[0], y = reinterpret_cast<const float4 *>(ml)[1];
-      m[0] = x.x; l[0] = x.y; m[1] = x.z; l[1] = x.w;
-      m[2] = y.x; l[2] = y.y; m[3] = y.z; l[3] = y.w;
+      const float4 x = ml ? ml[k] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      m[k] = x.x;
+      l[k] = x.y;
+      r[k] = x.z;
     }
   };
   // the job is the CTA's first one unless the CTA began with an earlier job
   auto slot_of = [&](const Deal &deal, int32_t c, int32_t start) { return 2 * c + (deal.start(c) < start ? 1 : 0); };
-  auto write = [&](const Split &sj, int h, int d0, float M, float L, float A) {  // head h of the job's group
+  auto write = [&](const Split &sj, int h, int d0, float M, float L, float R, float A) {  // head h of the job's group
     const int32_t bt = sj.job >> jobs.group_shift, group = sj.job & ((1 << jobs.group_shift) - 1);
     if (group * kH + h >= a.H) return;
     const int64_t row = static_cast<int64_t>(bt) * a.H + group * kH + h;
-    static_cast<__nv_bfloat16 *>(a.out)[row * kD + d0 + lane] = __float2bfloat16_rn(A * (L == 0.f ? 0.f : 1.f / L));
+    static_cast<__nv_bfloat16 *>(a.out)[row * kD + d0 + lane] = __float2bfloat16_rn(A * (R == 0.f ? 0.f : 1.f / R));
     if (a.lse && d0 == 0 && lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
   };
 
@@ -877,7 +893,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const l
     const int h4 = (item % (kItems / 4)) / 4, d0 = 128 * (item % 4);
     const Deal deal(sj.total, jobs.G);
     const int32_t from = deal.owner(sj.start), last = deal.owner(sj.end - 1);
-    float M[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, L[4] = {0.f, 0.f, 0.f, 0.f}, A[4][4] = {};
+    float M[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, L[4] = {0.f, 0.f, 0.f, 0.f}, R[4] = {0.f, 0.f, 0.f, 0.f}, A[4][4] = {};
 #pragma unroll 1
     for (int32_t c = from; c <= last; c++) {
       look(ws.ml + slot_of(deal, c, sj.start) * kH + 4 * h4);
@@ -895,6 +911,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const l
       for (int k = 0; k < 4; k++) {
         const float e0 = weight_of(m[k], M[k]);
         L[k] = fmaf(e0, l[k], L[k]);
+        R[k] = fmaf(e0, r[k], R[k]);
 #pragma unroll
         for (int j = 0; j < 4; j++) A[k][j] = fmaf(e0, reinterpret_cast<const float *>(&v[j])[k], A[k][j]);
       }
@@ -902,7 +919,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const l
 #pragma unroll
     for (int k = 0; k < 4; k++)
 #pragma unroll
-      for (int j = 0; j < 4; j++) write(sj, 4 * h4 + k, d0 + 32 * j, M[k], L[k], A[k][j]);
+      for (int j = 0; j < 4; j++) write(sj, 4 * h4 + k, d0 + 32 * j, M[k], L[k], R[k], A[k][j]);
   }
 
 #pragma unroll 1
@@ -912,7 +929,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const l
     const Deal deal(sj.total, jobs.G);
     const int32_t from = deal.owner(sj.start), n = deal.owner(sj.end - 1) - from + 1;  // <= kMaxCtas
     look(tid < n ? ws.ml + slot_of(deal, from + tid, sj.start) * kH + 4 * h4 : nullptr);
-    float M[4], L[4];
+    float M[4], L[4], R[4];
 #pragma unroll
     for (int k = 0; k < 4; k++) M[k] = warp_max(m[k]);
     if (lane == 0) red_s[0][warp] = make_float4(M[0], M[1], M[2], M[3]);
@@ -925,9 +942,13 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const l
     for (int k = 0; k < 4; k++) {
       e[k] = tid < n ? weight_of(m[k], M[k]) : 0.f;
       L[k] = warp_sum(tid < n ? e[k] * l[k] : 0.f);
+      R[k] = warp_sum(tid < n ? e[k] * r[k] : 0.f);
     }
     if (tid < n) weight_s[tid] = make_float4(e[0], e[1], e[2], e[3]);
-    if (lane == 0) red_s[1][warp] = make_float4(L[0], L[1], L[2], L[3]);
+    if (lane == 0) {
+      red_s[1][warp] = make_float4(L[0], L[1], L[2], L[3]);
+      red_s[2][warp] = make_float4(R[0], R[1], R[2], R[3]);
+    }
     __syncthreads();
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
@@ -942,13 +963,14 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const l
     acc_s[warp][lane] = acc;
     __syncthreads();
     if (warp < 4) {  // warp k finishes head k
-      float A = 0.f, Ls = 0.f;
+      float A = 0.f, Ls = 0.f, Rs = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; w++) {
         A += reinterpret_cast<const float *>(&acc_s[w][lane])[warp];
         Ls += reinterpret_cast<const float *>(&red_s[1][w])[warp];
+        Rs += reinterpret_cast<const float *>(&red_s[2][w])[warp];
       }
-      write(sj, 4 * h4 + warp, d0, warp == 0 ? M[0] : warp == 1 ? M[1] : warp == 2 ? M[2] : M[3], Ls, A);
+      write(sj, 4 * h4 + warp, d0, warp == 0 ? M[0] : warp == 1 ? M[1] : warp == 2 ? M[2] : M[3], Ls, Rs, A);
     }
     __syncthreads();
   }
@@ -1000,7 +1022,7 @@ bool paged_attn_supported(const lidx_paged_attn_args &a) {
 
 size_t paged_attn_workspace(const lidx_paged_attn_args &a) {
   const Jobs j = plan(a);
-  return LIDX_WS_HEADER + align256(j.G * sizeof(Split)) + static_cast<size_t>(j.G) * 2 * kH * (8 + kD * 4);
+  return LIDX_WS_HEADER + align256(j.G * sizeof(Split)) + static_cast<size_t>(j.G) * 2 * kH * (sizeof(float4) + kD * 4);
 }
 
 int paged_attn_launches(const lidx_paged_attn_args &) { return 2; }  // the attention and the merge
@@ -1013,8 +1035,8 @@ cudaError_t launch_paged_attn(const lidx_paged_attn_args &a, void *ws, cudaStrea
   p += LIDX_WS_HEADER;
   s.split = reinterpret_cast<Split *>(p);
   p += align256(j.G * sizeof(Split));
-  s.ml = reinterpret_cast<float2 *>(p);
-  p += static_cast<size_t>(j.G) * 2 * kH * 8;
+  s.ml = reinterpret_cast<float4 *>(p);
+  p += static_cast<size_t>(j.G) * 2 * kH * sizeof(float4);
   s.o = reinterpret_cast<float4 *>(p);
   CUtensorMap tm;
   if (!make_tmap_3d(&tm, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kD, a.H, static_cast<uint64_t>(a.B) * a.T, 64, kH,
