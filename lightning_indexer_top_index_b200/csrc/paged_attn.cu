@@ -8,30 +8,35 @@
 // job may span CTAs.  A job that one CTA holds whole is written out by it; the
 // others leave partial results (m, l, O) that the merge kernel joins.
 //
-// A CTA has 14 warps:
+// A CTA has 19 warps:
 //   * the scout finds each chunk's pool rows (block list, page table) up to
 //     four chunks ahead and says where a job begins and ends;
-//   * eight loader warps, one per 64-dim slab of the row, fetch the stored
-//     rows a chunk ahead into registers, expand them to bf16 (exact: every
-//     E2M1 or E4M3 value times a power of two is a bf16 value) and store them
-//     as the swizzled K-major tile X[64 rows][512], two of which are in shared
-//     memory.  Rows that are not attended to are stored as zeros;
-//   * one thread issues S[head][row] = Q . X^T (M = 64, N = 64, K = 512) and,
-//     when the chunk's probabilities are there, O^T[d][head] += X^T . P^T
-//     (M = 128 four times, N = 64, K = 64), both on tcgen05 with fp32
-//     accumulators in TMEM.  Products that add to the same accumulator wait
-//     for one another, so S is summed in four parts (K quarters) and O's four
-//     dim tiles are taken in turn;
-//   * four softmax warps read S in the 16x256b shape, in which the 32 lanes of
-//     a warp share the 16 heads of its TMEM quarter (8 head pairs x 4 column
-//     groups), so row maxima take two shuffles and no lane idles.  S is free
-//     for the next chunk as soon as it is read.  The running maximum is only a
+//   * eight loader warps, eight rows each, fetch the stored rows a chunk ahead
+//     into registers, expand them to bf16 (exact: every E2M1 or E4M3 value
+//     times a power of two is a bf16 value) and store them as the swizzled
+//     K-major tile X[64 rows][512], two of which are in shared memory.  Rows
+//     that are not attended to are stored as zeros.  They go by quarters of 128
+//     dims, and S begins with the half of the dims that is in while the other
+//     is expanded; a half is refilled once O is done with its dims.  So the
+//     stages of a chunk, whose lengths add up to the CTA's pace, overlap;
+//   * one warp issues S[head][row] = Q . X^T (M = 64, N = 64, K = 512) and
+//     another, when the chunk's probabilities are there, O^T[d][head] +=
+//     X^T . P^T (M = 128 four times, N = 64, K = 64), both on tcgen05 with fp32
+//     accumulators in TMEM, two of S and one of O.  (One warp that polled for
+//     whichever was ready cost 300 to 700 cycles a product: 123 against 102 us
+//     for 256 queries of 1024 rows.  S in two or four accumulators, whose
+//     products need not wait for one another, cost the softmax warps as much as
+//     it gained: 104 us.);
+//   * eight softmax warps, one per 16 heads and half of the chunk's rows, read
+//     S in the 16x256b shape, in which the 32 lanes of a warp share the 16 heads
+//     of its TMEM quarter (8 head pairs x 4 column groups), so row maxima take
+//     two shuffles and no lane idles.  The running maximum is only a
 //     reference (p = 2^(s - m) may exceed 1), so it moves only when it rises
 //     by more than 32 (base 2), and only then is the O so far rescaled in
 //     TMEM: at 8 one of the 64 heads made most chunks pay for it.  Sums are of
 //     the fp32 probabilities; floating point loses nothing by a common factor
 //     up to 2^32.
-//   P is rounded to bf16 for the second product, 2^-9 of each probability.  O
+//   P is rounded to bf16 for the second product, at most 2^-8 of each probability.  O
 //   is divided by the sum of the rounded ones, so that its weights add up to
 //   one and a row that has nearly all of it comes out exactly (by the unrounded
 //   sum the error over peaked rows was 1.6 times that of an exact P); lse takes
@@ -53,24 +58,24 @@ namespace {
 constexpr int kD = 512;
 constexpr int kH = 64;                   // heads of a job
 constexpr int kRows = 64;                // rows of a chunk
-constexpr int kLoaders = 8;              // warps; warp i of them fills dims [64 i, 64 i + 64)
-constexpr int kSoftmaxWarps = 4;
-constexpr int kThreads = 32 * (kSoftmaxWarps + kLoaders + 2);
-constexpr int kMma = kSoftmaxWarps + kLoaders, kScout = kMma + 1;  // their warps
+constexpr int kLoaders = 8;              // warps, eight rows each
+constexpr int kSoftmaxWarps = 8;         // warp w: heads 16 (w % 4) .., rows 32 (w / 4) .. of a chunk
+constexpr int kThreads = 32 * (kSoftmaxWarps + kLoaders + 3);
+constexpr int kIssueS = kSoftmaxWarps + kLoaders, kIssueO = kIssueS + 1, kScout = kIssueO + 1;  // their warps
 constexpr int kRing = 4;                 // chunks the scout may be ahead
 constexpr int kPanel = 64 * 128;         // one 64-line panel of X or Q: 64 dims
 constexpr int kXBytes = 8 * kPanel;
 constexpr int kQBytes = 8 * kPanel;
 constexpr int kPBytes = kH * kRows * 2;
-constexpr int kParts = 4;                // partial sums of S, at columns 64 i
-constexpr uint32_t kOCol = 64 * kParts;  // O^T tile t at columns kOCol + 64 t
+constexpr uint32_t kOCol = 128;          // S of stage i at columns 64 i, O^T tile t at columns kOCol + 64 t
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 32.f;            // base-2 headroom of the reference maximum
 constexpr int kMergeThreads = 256;
 constexpr int kFew = 8;                  // partials that one warp joins
+constexpr int kBatch = 10;               // partials that a warp of the merge has in flight: two batches of 148 / 8
+constexpr int kMergeCtas = 4;            // of the merge, for an SM
 constexpr int kMaxCtas = 256;            // one CTA per SM
-constexpr uint32_t kIdleLimit = 1u << 24;  // rounds without work after which the issuing warp gives up (seconds)
 
 // What the scout says about a chunk.
 constexpr uint32_t kFirst = 1u;  // the first chunk of its job in this CTA
@@ -87,14 +92,17 @@ struct __align__(16) Smem {
   Chunk ring[kRing];
   uint64_t ring_full[kRing], ring_free[kRing];
   uint64_t q_full;
-  uint64_t x_full[2], x_free[2];  // a stage's rows are in / its second product is done (X and P free again)
-  uint64_t s_full, s_free;
+  uint64_t x_full[2][2];          // half of the dims of a stage's rows are in
+  uint64_t x_free[2][2];          // the second product is done with half of its dims (with the second half: and with P)
+  uint64_t s_full[2];
   uint64_t p_full[2];
   uint64_t o_free;                // the finished job's O has been read
-  uint64_t drained;               // every product issued is done (only after a wait gave up)
+  uint64_t drained[2];            // every S or O product issued is done (only after a wait gave up)
   uint32_t tmem_base;
   uint32_t abort;
-  float alpha[2][kH];             // rescale factors of a chunk
+  float alpha[kH];                // rescale factors of a chunk
+  float top[2][kH];               // a chunk's maxima, by half of its rows
+  float sums[2][kH][2];           // a job's sums, by half of the rows
   float l[kH];                    // 1 / sum of the rounded probabilities
   // the CTA's first chunk
   int32_t job, chunk;
@@ -158,24 +166,6 @@ __device__ __forceinline__ bool elect() {  // true in one lane of a converged wa
   return r != 0u;
 }
 
-// Whether the phase with `parity` has completed, without waiting.
-__device__ __forceinline__ bool test(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n"
-      " .reg .pred p;\n"
-      " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n"
-      "}\n"
-      : "=r"(ok)
-      : "r"(tc::smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0u;
-}
-__device__ __forceinline__ bool ready(uint64_t *bar, uint32_t parity) {  // the same answer in all lanes
-  return __all_sync(0xFFFFFFFFu, test(bar, parity));
-}
-
 // tc::mbar_wait with its loop kept rolled.
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile uint32_t *abort) {
 #pragma unroll 1
@@ -185,6 +175,11 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatil
   }
   *abort = 1u;
   return false;
+}
+
+// A whole warp waits: the same answer in all lanes.
+__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, volatile uint32_t *abort) {
+  return __all_sync(0xFFFFFFFFu, wait_for(bar, parity, abort));
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {  // 2 ulp; 2^-inf = 0
@@ -208,18 +203,31 @@ __device__ __forceinline__ uint32_t bar_or(int id, int n, uint32_t v) {
   return r;
 }
 
-// S of 16 heads x 64 rows: lane l holds heads l/4 (regs 4u, 4u+1) and l/4 + 8
+// S of 16 heads x 32 rows: lane l holds heads l/4 (regs 4u, 4u+1) and l/4 + 8
 // (regs 4u+2, 4u+3), rows 8u + 2 (l % 4) and the next.
-__device__ __forceinline__ void tmem_ld_s(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_s(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+// 16 consecutive columns of this thread's lane, without waiting.
+__device__ __forceinline__ void tmem_ld16_issue(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_pin16(uint32_t (&r)[16]) {  // no use of them before the wait above this
+#pragma unroll
+  for (int i = 0; i < 16; i += 8)
+    asm volatile(""
+                 : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                   "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
@@ -245,71 +253,47 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *m, uin
       : "memory");
 }
 
-// Stored bytes of one 64-dim slab: 16-byte pieces a row, and the dims a piece holds.
+// A quarter (128 dims, two panels of X) of a row in 16-byte pieces as stored;
+// a loader warp's eight rows of it are kIters pieces a lane.
 template <int kFmt>
 struct Fmt {
-  static constexpr int kPieces = kFmt == LIDX_E2M1 ? 2 : kFmt == LIDX_E4M3 ? 4 : 8;
-  static constexpr int kIters = kRows * kPieces / 32;       // pieces a lane loads
+  static constexpr int kPieces = kFmt == LIDX_E2M1 ? 4 : kFmt == LIDX_E4M3 ? 8 : 16;
+  static constexpr int kIters = kPieces / 4;
   static constexpr int kRowsPerIter = 32 / kPieces;
 };
 
-// One 64-dim slab of a chunk (or kIters * kRowsPerIter rows of it, from row
-// `from` on) in registers: piece it of a lane is piece lane % kPieces of row
-// from + it * kRowsPerIter + lane / kPieces.
-template <int kFmt, int kIters = Fmt<kFmt>::kIters>
-struct Slab {
-  uint4 v[kIters];
-  uint32_t scale[kFmt == LIDX_BF16 ? 1 : kIters];
-
-  // rows: the chunk's pool rows in shared memory
-  __device__ __forceinline__ void load(const void *plane, int64_t ld, const uint8_t *scales, int64_t ld_scale, int slab,
-                                       int lane, const int32_t *rows, int from) {
-    using F = Fmt<kFmt>;
-    const uint8_t *base = static_cast<const uint8_t *>(plane) + slab * (F::kPieces * 16) + (lane % F::kPieces) * 16;
-    const int64_t pitch = kFmt == LIDX_BF16 ? 2 * ld : ld;
+// Piece p of row r expanded to bf16 into the quarter's panels at x.  Lanes of
+// the second panel take their 16-byte chunks in another order, so that the
+// eight lanes that store together hit all banks.
+template <int kFmt>
+__device__ __forceinline__ void store_piece(uint8_t *x, int r, int p, const uint4 &v, uint32_t scale, bool on) {
+  uint8_t *row = x + r * 128 + (p / (Fmt<kFmt>::kPieces / 2)) * kPanel;
+  const int swz = r & 7;
+  if constexpr (kFmt == LIDX_BF16) {
+    if (on) *reinterpret_cast<uint4 *>(row + (((p & 7) ^ swz) << 4)) = v;
+  } else if constexpr (kFmt == LIDX_E2M1) {
+    const int turn = p & 2;
+    const uint32_t w[4] = {turn ? v.z : v.x, turn ? v.w : v.y, turn ? v.x : v.z, turn ? v.y : v.w};
+    const E2m1Scale s(scale);
 #pragma unroll
-    for (int it = 0; it < kIters; it++) {
-      const int32_t p = rows[from + it * F::kRowsPerIter + lane / F::kPieces];
-      v[it] = make_uint4(0, 0, 0, 0);
-      if (kFmt != LIDX_BF16) scale[it] = 127u;
-      if (p >= 0) {
-        v[it] = __ldg(reinterpret_cast<const uint4 *>(base + p * pitch));
-        if (kFmt == LIDX_E2M1) scale[it] = __ldg(scales + p * ld_scale + slab * 2 + lane % 2);
-        if (kFmt == LIDX_E4M3) scale[it] = __ldg(scales + p * ld_scale + slab);
-      }
+    for (int i = 0; i < 4; i++) {
+      uint32_t o[4];
+      s.expand(w[i], o);
+      if (on) *reinterpret_cast<uint4 *>(row + (((4 * (p & 1) + (i ^ turn)) ^ swz) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  } else {
+    const int turn = (p >> 2) & 1;
+    const uint32_t w[4] = {turn ? v.z : v.x, turn ? v.w : v.y, turn ? v.x : v.z, turn ? v.y : v.w};
+    const uint32_t s = e8m0_to_bf16x2(scale);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const uint4 o = make_uint4(mul_bf16x2(e4m3x2_to_bf16x2(w[2 * i]), s), mul_bf16x2(e4m3x2_to_bf16x2(w[2 * i] >> 16), s),
+                                 mul_bf16x2(e4m3x2_to_bf16x2(w[2 * i + 1]), s),
+                                 mul_bf16x2(e4m3x2_to_bf16x2(w[2 * i + 1] >> 16), s));
+      if (on) *reinterpret_cast<uint4 *>(row + (((2 * (p & 3) + (i ^ turn)) ^ swz) << 4)) = o;
     }
   }
-
-  // expanded to bf16 into the slab's panel of X
-  __device__ __forceinline__ void store(uint8_t *panel, int lane, int from) const {
-    using F = Fmt<kFmt>;
-#pragma unroll
-    for (int it = 0; it < kIters; it++) {
-      const int r = from + it * F::kRowsPerIter + lane / F::kPieces, piece = lane % F::kPieces;
-      uint8_t *row = panel + r * 128;
-      const uint32_t w[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
-      if (kFmt == LIDX_BF16) {
-        *reinterpret_cast<uint4 *>(row + ((piece ^ (r & 7)) << 4)) = v[it];
-      } else if (kFmt == LIDX_E2M1) {
-        const E2m1Scale s(scale[it]);
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          uint32_t o[4];
-          s.expand(w[i], o);
-          *reinterpret_cast<uint4 *>(row + (((4 * piece + i) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-      } else {
-        const uint32_t s = e8m0_to_bf16x2(scale[it]);
-#pragma unroll
-        for (int i = 0; i < 2; i++)
-          *reinterpret_cast<uint4 *>(row + (((2 * piece + i) ^ (r & 7)) << 4)) =
-              make_uint4(mul_bf16x2(e4m3x2_to_bf16x2(w[2 * i]), s), mul_bf16x2(e4m3x2_to_bf16x2(w[2 * i] >> 16), s),
-                         mul_bf16x2(e4m3x2_to_bf16x2(w[2 * i + 1]), s),
-                         mul_bf16x2(e4m3x2_to_bf16x2(w[2 * i + 1] >> 16), s));
-      }
-    }
-  }
-};
+}
 
 // Pool row of entry e of a job's row list, or -1.
 __device__ __forceinline__ int32_t entry_row(const lidx_paged_attn_args &a, int32_t bt, int shift, int32_t e,
@@ -350,18 +334,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int i = 0; i < kRing; i++) {
       tc::mbar_init(&sm->ring_full[i], 1);
-      tc::mbar_init(&sm->ring_free[i], kSoftmaxWarps + kLoaders + 1);
+      tc::mbar_init(&sm->ring_free[i], kSoftmaxWarps + kLoaders + 2);
     }
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-      tc::mbar_init(&sm->x_full[i], kLoaders);
-      tc::mbar_init(&sm->x_free[i], 1);
+#pragma unroll
+      for (int h = 0; h < 2; h++) tc::mbar_init(&sm->x_full[i][h], kLoaders);
+      tc::mbar_init(&sm->x_free[i][0], 1);
+      tc::mbar_init(&sm->x_free[i][1], 1);
       tc::mbar_init(&sm->p_full[i], kSoftmaxWarps);
+      tc::mbar_init(&sm->s_full[i], 1);
     }
-    tc::mbar_init(&sm->s_full, 1);
-    tc::mbar_init(&sm->s_free, kSoftmaxWarps);
     tc::mbar_init(&sm->o_free, kSoftmaxWarps);
-    tc::mbar_init(&sm->drained, 1);
+    tc::mbar_init(&sm->drained[0], 1);
+    tc::mbar_init(&sm->drained[1], 1);
     sm->abort = 0;
     tc::fence_barrier_init();
     tc::tma_prefetch_desc(&tm_q);
@@ -478,130 +464,180 @@ __global__ void __launch_bounds__(kThreads, 1)
       left--;
     }
     if (bounds) raise_status(ws.status, LIDX_DEV_BOUNDS);
-  } else if (warp >= kSoftmaxWarps && warp < kMma) {
+  } else if (warp >= kSoftmaxWarps && warp < kIssueS) {
     // ------------------------------------------------------------ loaders
-    const int slab = warp - kSoftmaxWarps;
-    const lidx_kv &kv = a.cache.rows;
+    using F = Fmt<kFmt>;
     constexpr bool kQuant = kFmt != LIDX_BF16;
-    Slab<kFmt> part;
-    Slab<LIDX_BF16, 2> rope;  // the quantised formats' RoPE dims: eight rows a warp
+    const lidx_kv &kv = a.cache.rows;
+    const int from = 8 * (warp - kSoftmaxWarps);  // the warp's rows of a chunk
+    const int piece = lane % F::kPieces;
+    const uint8_t *data = static_cast<const uint8_t *>(kv.data) + piece * 16;
+    const int64_t pitch = kFmt == LIDX_BF16 ? 2 * kv.ld : kv.ld;
+    const uint8_t *scales = kv.scale + (kFmt == LIDX_E2M1 ? piece : piece / 4);
+    const uint8_t *rope = static_cast<const uint8_t *>(kv.rope) + (lane % 8) * 16;
+    const bool in_last = !kQuant || piece < F::kPieces / 2;  // the last quarter has codes for its first panel only
+    uint4 v[4][F::kIters], rv[2];
+    uint32_t sc[4][F::kIters];
 #pragma unroll 1
-    for (int i = 0; i <= n; i++) {  // chunk i - 1 into shared memory, chunk i into registers
-      if (i > 0) {
-        const int stage = (i - 1) & 1;
-        if (i > 2 && !warp_wait(&sm->x_free[stage], (((i - 1) >> 1) - 1) & 1)) break;
-        uint8_t *x = sX + stage * kXBytes;
-        if (!kQuant || slab < 7) part.store(x + slab * kPanel, lane, 0);
-        if (kQuant) rope.store(x + 7 * kPanel, lane, 8 * slab);
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm->x_full[stage]);
-      }
+    for (int i = 0; i <= n; i++) {  // chunk i - 1 into shared memory, chunk i into registers, a quarter at a time
+      int32_t row[F::kIters], rope_row[2];
       if (i < n) {
         const int slot = i % kRing;
         if (!warp_wait(&sm->ring_full[slot], (i / kRing) & 1)) break;
-        const int32_t *rows = sm->ring[slot].row;
-        if (!kQuant || slab < 7) part.load(kv.data, kv.ld, kv.scale, kv.ld_scale, slab, lane, rows, 0);
-        if (kQuant) rope.load(kv.rope, kv.ld_rope, nullptr, 0, 0, lane, rows, 8 * slab);
+        const int32_t *rows = sm->ring[slot].row + from;
+#pragma unroll
+        for (int it = 0; it < F::kIters; it++) row[it] = rows[it * F::kRowsPerIter + lane / F::kPieces];
+#pragma unroll
+        for (int it = 0; it < 2; it++) rope_row[it] = rows[it * 4 + lane / 8];
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm->ring_free[slot]);
       }
+      const int stage = (i - 1) & 1;
+      bool ok = true;
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        if (i > 0 && ok) {
+          if (i > 2 && (q & 1) == 0) ok = warp_wait(&sm->x_free[stage][q >> 1], (((i - 1) >> 1) - 1) & 1);
+          if (!ok) break;
+          uint8_t *x = sX + stage * kXBytes + 2 * q * kPanel;
+#pragma unroll
+          for (int it = 0; it < F::kIters; it++)
+            store_piece<kFmt>(x, from + it * F::kRowsPerIter + lane / F::kPieces, piece, v[q][it], sc[q][it], q < 3 || in_last);
+          if (kQuant && q == 3) {
+#pragma unroll
+            for (int it = 0; it < 2; it++)
+              store_piece<LIDX_BF16>(x + kPanel, from + it * 4 + lane / 8, lane % 8, rv[it], 0u, true);
+          }
+          if (q & 1) {
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sm->x_full[stage][q >> 1]);
+          }
+        }
+        if (i < n) {
+#pragma unroll
+          for (int it = 0; it < F::kIters; it++) {
+            v[q][it] = make_uint4(0, 0, 0, 0);
+            sc[q][it] = 127u;
+            if (row[it] >= 0 && (q < 3 || in_last)) {
+              v[q][it] = __ldg(reinterpret_cast<const uint4 *>(data + row[it] * pitch + q * (F::kPieces * 16)));
+              if (kQuant) sc[q][it] = __ldg(scales + row[it] * kv.ld_scale + q * (kFmt == LIDX_E2M1 ? 4 : 2));
+            }
+          }
+          if (kQuant && q == 3) {
+#pragma unroll
+            for (int it = 0; it < 2; it++) {
+              rv[it] = make_uint4(0, 0, 0, 0);
+              if (rope_row[it] >= 0) rv[it] = __ldg(reinterpret_cast<const uint4 *>(rope + rope_row[it] * 2 * kv.ld_rope));
+            }
+          }
+        }
+      }
+      if (!ok) break;
     }
-  } else if (warp == kMma) {
-    // ------------------------------------------------- the matrix products
+  } else if (warp == kIssueS) {
+    // ------------------------------------------------- S = Q . X^T
     // The whole warp goes through the loop, so that descriptors and flags stay
     // in uniform registers, and one elected lane issues: with a single lane in
     // the loop each product took 100 cycles to issue, whatever its shape.
-    const uint32_t idesc_s = tc::idesc_bf16(64, 64), idesc_o = tc::idesc_bf16(128, 64, true, false);
+    const uint32_t idesc = tc::idesc_bf16(64, 64);
     const uint64_t q_desc = tc::desc_kmajor_sw128(tc::smem_u32(sQ));
     const uint64_t x_desc = tc::desc_kmajor_sw128(tc::smem_u32(sX));
-    const uint64_t xt_desc = tc::desc_mnmajor_sw128(tc::smem_u32(sX), kPanel, 1024);
-    const uint64_t p_desc = tc::desc_kmajor_sw128(tc::smem_u32(sP));
-    int si = 0, oi = 0;                  // the next chunk of S and of O
-    int s_jobs = 0, o_jobs = 0;          // jobs begun by then
-    uint32_t firsts = 0u;                // bit i % 2: chunk i is the first of its job
-    int state = 0;                       // of chunk si: 0 unknown, 1 known and Q wanted, 2 Q on its way, 3 Q there
-    uint32_t idle = 0;
+    int begun = 0;  // jobs
+    bool ok = true, q_there = true;
 #pragma unroll 1
-    while (oi < n) {
-      bool moved = false;
-      if (si < n && si < oi + 2) {
-        if (state == 0 && ready(&sm->ring_full[si % kRing], (si / kRing) & 1)) {
-          const Chunk &k = sm->ring[si % kRing];
-          state = (k.flags & kFirst) ? 1 : 3;
-          firsts = (firsts & ~(1u << (si & 1))) | ((k.flags & kFirst) << (si & 1));
-          if (state == 3) {
-            __syncwarp();
-            if (elect()) tc::mbar_arrive(&sm->ring_free[si % kRing]);
-          }
-        }
-        if (state == 1 && (si == 0 || ready(&sm->s_full, (si - 1) & 1))) {  // Q has been read for the last time
-          const int32_t job = sm->ring[si % kRing].job;
-          __syncwarp();
-          if (elect()) {
-            tc::mbar_arrive(&sm->ring_free[si % kRing]);
-            tc::mbar_arrive_expect_tx(&sm->q_full, kQBytes);
+    for (int i = 0; i < n && ok; i++) {
+      const int slot = i % kRing;
+      ok = wait_all(&sm->ring_full[slot], (i / kRing) & 1, abort_flag);
+      if (!ok) break;
+      if (sm->ring[slot].flags & kFirst) {  // a new job's Q, when the last one has been read for the last time
+        if (i > 0) ok = wait_all(&sm->s_full[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag);
+        if (!ok) break;
+        const int32_t job = sm->ring[slot].job;
+        if (elect()) {
+          tc::mbar_arrive_expect_tx(&sm->q_full, kQBytes);
 #pragma unroll 1
-            for (int p = 0; p < 8; p++)
-              tma_load_3d(sQ + p * kPanel, &tm_q, &sm->q_full, 64 * p, (job & ((1 << gs) - 1)) * kH, job >> gs);
-          }
-          __syncwarp();
-          s_jobs++;
-          state = 2;
+          for (int p = 0; p < 8; p++)
+            tma_load_3d(sQ + p * kPanel, &tm_q, &sm->q_full, 64 * p, (job & ((1 << gs) - 1)) * kH, job >> gs);
         }
-        if (state == 2 && ready(&sm->q_full, (s_jobs - 1) & 1)) state = 3;
-        if (state == 3 && ready(&sm->x_full[si & 1], (si >> 1) & 1) && (si == 0 || ready(&sm->s_free, (si - 1) & 1))) {
-          tc::tc_fence_after();
-          // step k: panel k / 4, 32 bytes (k % 4) into it; part p sums panels 2p and 2p + 1
-          const uint64_t xd = x_desc + (si & 1) * (kXBytes >> 4);
-          if (elect()) {
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-#pragma unroll
-              for (int part = 0; part < kParts; part++) {
-                const uint32_t off = (2 * part + (j >> 2)) * (kPanel >> 4) + (j & 3) * 2;
-                tc::mma_bf16(tmem + 64 * part, q_desc + off, xd + off, idesc_s, j > 0);
-              }
-            }
-            tc::mma_commit(&sm->s_full);
-          }
-          __syncwarp();
-          si++;
-          state = 0;
-          moved = true;
-        }
+        __syncwarp();
+        begun++;
+        q_there = false;
       }
-      if (oi < si && ready(&sm->p_full[oi & 1], (oi >> 1) & 1)) {
-        const bool first = (firsts >> (oi & 1)) & 1u;
-        if (!first || o_jobs == 0 || ready(&sm->o_free, (o_jobs - 1) & 1)) {
-          tc::tc_fence_after();
-          const uint64_t xd = xt_desc + (oi & 1) * (kXBytes >> 4), pd = p_desc + (oi & 1) * (kPBytes >> 4);
-          if (elect()) {
-#pragma unroll
-            for (int kk = 0; kk < kRows / 16; kk++) {
-#pragma unroll
-              for (int dt = 0; dt < 4; dt++)
-                tc::mma_bf16(tmem + kOCol + 64 * dt, xd + ((2 * dt * kPanel + kk * 2048) >> 4), pd + kk * 2, idesc_o,
-                             !first || kk > 0);
-            }
-            tc::mma_commit(&sm->x_free[oi & 1]);
-          }
-          __syncwarp();
-          o_jobs += first;
-          oi++;
-          moved = true;
-        }
+      if (!q_there) {
+        q_there = wait_all(&sm->q_full, (begun - 1) & 1, abort_flag);
+        ok = ok && q_there;
       }
-      idle = moved ? 0u : idle + 1u;
-      if (idle > kIdleLimit) *abort_flag = 1u;
-      if (__any_sync(0xFFFFFFFFu, *abort_flag != 0u)) break;
+#pragma unroll 1
+      for (int h = 0; h < 2 && ok; h++) {  // as the halves of the rows come in
+        ok = wait_all(&sm->x_full[i & 1][h], (i >> 1) & 1, abort_flag);
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint64_t qd = q_desc + 4 * h * (kPanel >> 4), xd = x_desc + (i & 1) * (kXBytes >> 4) + 4 * h * (kPanel >> 4);
+        if (elect()) {
+#pragma unroll
+          for (int j = 0; j < 16; j++) {  // panel j / 4, 32 bytes (j % 4) into it
+            const uint32_t off = (j >> 2) * (kPanel >> 4) + (j & 3) * 2;
+            tc::mma_bf16(tmem + 64 * (i & 1), qd + off, xd + off, idesc, h > 0 || j > 0);
+          }
+          if (h == 1) {
+            tc::mbar_arrive(&sm->ring_free[slot]);
+            tc::mma_commit(&sm->s_full[i & 1]);
+          }
+        }
+        __syncwarp();
+      }
     }
-    if (oi < n) {  // a wait gave up: the copies and products in flight end before the CTA does
+    if (!ok) {  // a wait gave up: the copies and products in flight end before the CTA does
       volatile uint32_t unused = 0;
-      if (state >= 2 && s_jobs > 0) wait_for(&sm->q_full, (s_jobs - 1) & 1, &unused);
-      if (elect()) tc::mma_commit(&sm->drained);
+      if (!q_there) wait_for(&sm->q_full, (begun - 1) & 1, &unused);
+      if (elect()) tc::mma_commit(&sm->drained[0]);
       __syncwarp();
-      wait_for(&sm->drained, 0, &unused);
+      wait_for(&sm->drained[0], 0, &unused);
+    }
+  } else if (warp == kIssueO) {
+    // ------------------------------------------------- O^T += X^T . P^T, by a warp of its own: neither product waits for the other's turn
+    const uint32_t idesc = tc::idesc_bf16(128, 64, true, false);
+    const uint64_t x_desc = tc::desc_mnmajor_sw128(tc::smem_u32(sX), kPanel, 1024);
+    const uint64_t p_desc = tc::desc_kmajor_sw128(tc::smem_u32(sP));
+    int begun = 0;  // jobs
+    bool ok = true;
+#pragma unroll 1
+    for (int i = 0; i < n && ok; i++) {
+      const int slot = i % kRing;
+      ok = wait_all(&sm->ring_full[slot], (i / kRing) & 1, abort_flag);
+      if (!ok) break;
+      const bool first = sm->ring[slot].flags & kFirst;
+      __syncwarp();
+      if (elect()) tc::mbar_arrive(&sm->ring_free[slot]);
+      if (first) {
+        if (begun > 0) ok = wait_all(&sm->o_free, (begun - 1) & 1, abort_flag);
+        begun++;
+      }
+      ok = ok && wait_all(&sm->p_full[i & 1], (i >> 1) & 1, abort_flag);
+      if (!ok) break;
+      tc::tc_fence_after();
+      const uint64_t xd = x_desc + (i & 1) * (kXBytes >> 4), pd = p_desc + (i & 1) * (kPBytes >> 4);
+      if (elect()) {
+        // two dim tiles at a time: the loaders may then refill their panels
+#pragma unroll
+        for (int dt = 0; dt < 4; dt += 2) {
+#pragma unroll
+          for (int kk = 0; kk < kRows / 16; kk++) {
+#pragma unroll
+            for (int k = dt; k < dt + 2; k++)
+              tc::mma_bf16(tmem + kOCol + 64 * k, xd + ((2 * k * kPanel + kk * 2048) >> 4), pd + kk * 2, idesc, !first || kk > 0);
+          }
+          tc::mma_commit(&sm->x_free[i & 1][dt / 2]);
+        }
+      }
+      __syncwarp();
+    }
+    if (!ok) {
+      volatile uint32_t unused = 0;
+      if (elect()) tc::mma_commit(&sm->drained[1]);
+      __syncwarp();
+      wait_for(&sm->drained[1], 0, &unused);
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -619,63 +655,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       cut_len(__ldg(a.len + bt / a.T), a.cache, cut);
       if (cut && tid == 0) raise_status(ws.status, LIDX_DEV_BOUNDS);
     }
-    const int h0 = warp * 16 + (lane >> 2), h1 = h0 + 8;  // this lane's heads
+    const int half = warp >> 2, h0 = (warp & 3) * 16 + (lane >> 2), h1 = h0 + 8;  // this lane's heads
     // logits are s * c2 in base 2; with a negative scale s changes sign instead, and a zero one
     // becomes one that makes every product round away (0 * -inf would be NaN)
     const bool negative = a.scale < 0.f;
     const float c2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
-    const uint32_t quarter = static_cast<uint32_t>(warp * 32) << 16;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, r0 = 0.f, r1 = 0.f;  // r: of the rounded probabilities
+    const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    // the reference maximum is the same in both halves; the sums are of this half's rows (r: of the
+    // rounded probabilities)
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, r0 = 0.f, r1 = 0.f;
     bool first_segment = true;  // the CTA's first job
+    bool fresh = true;          // nothing of the job is in O yet
+    uint32_t next_valid = 0u, next_flags = 0u;  // what the scout says about the next chunk
+    int32_t next_job = 0;
     // After a wait that gave up the warp goes through the rest of its chunks
     // without touching TMEM or global memory, for the others' barriers.
     bool ok = true;
-#pragma unroll 1
-    for (int i = 0; i < n; i++) {
-      const int stage = i & 1, slot = i % kRing;
+    auto look_ahead = [&](int i) {
+      if (i >= n) return;
+      const int slot = i % kRing;
       ok = warp_wait(&sm->ring_full[slot], (i / kRing) & 1) && ok;
-      const uint32_t v0 = sm->ring[slot].valid[0], v1 = sm->ring[slot].valid[1];
-      const int32_t job = sm->ring[slot].job;
-      const uint32_t flags = ok ? sm->ring[slot].flags : 0u;
+      next_valid = sm->ring[slot].valid[half];
+      next_job = sm->ring[slot].job;
+      next_flags = ok ? sm->ring[slot].flags : 0u;
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm->ring_free[slot]);
-      ok = warp_wait(&sm->s_full, i & 1) && ok;
-      float s0[16], s1[16];
+    };
+    look_ahead(0);
+#pragma unroll 1
+    for (int i = 0; i < n; i++) {
+      const int stage = i & 1;
+      const uint32_t valid = next_valid, flags = next_flags;
+      const int32_t job = next_job;
+      ok = warp_wait(&sm->s_full[stage], (i >> 1) & 1) && ok;
+      float s0[8], s1[8];
       if (ok) {
         tc::tc_fence_after();
-        uint32_t x[32], y[32];
-#pragma unroll
-        for (int part = 0; part < kParts; part += 2) {
-          tmem_ld_s(tmem + quarter + 64 * part, x);
-          tmem_ld_s(tmem + quarter + 64 * (part + 1), y);
-          tc::tmem_ld_wait();
-          tc::tmem_ld32_pin(x);
-          tc::tmem_ld32_pin(y);
-#pragma unroll
-          for (int u = 0; u < 16; u++) {
-            const int k = 4 * (u >> 1) + (u & 1);
-            const float p = __uint_as_float(x[k]) + __uint_as_float(y[k]);
-            const float q = __uint_as_float(x[k + 2]) + __uint_as_float(y[k + 2]);
-            s0[u] = part ? s0[u] + p : p;
-            s1[u] = part ? s1[u] + q : q;
-          }
-        }
+        uint32_t x[16];
+        tmem_ld_s(tmem + quarter + 64 * stage + 32 * half, x);
+        tc::tmem_ld_wait();
+        tmem_pin16(x);
         tc::tc_fence_before();
-      }
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm->s_free);
-      float t0 = -INFINITY, t1 = -INFINITY;
-      if (negative || (v0 & v1) != 0xFFFFFFFFu) {
 #pragma unroll
-        for (int u = 0; u < 16; u++) {  // row 8 (u / 2) + 2 (lane % 4) + u % 2
-          const uint32_t bits = (u < 8 ? v0 : v1) >> (2 * (lane & 3));
-          const bool in = (bits >> (8 * ((u >> 1) & 3) + (u & 1))) & 1u;
+        for (int u = 0; u < 8; u++) {  // row 8 (u / 2) + 2 (lane % 4) + u % 2 of the half
+          const int k = 4 * (u >> 1) + (u & 1);
+          s0[u] = __uint_as_float(x[k]);
+          s1[u] = __uint_as_float(x[k + 2]);
+        }
+      }
+      if (negative || valid != 0xFFFFFFFFu) {
+        const uint32_t bits = valid >> (2 * (lane & 3));
+#pragma unroll
+        for (int u = 0; u < 8; u++) {
+          const bool in = (bits >> (8 * (u >> 1) + (u & 1))) & 1u;
           s0[u] = in ? (negative ? -s0[u] : s0[u]) : -INFINITY;
           s1[u] = in ? (negative ? -s1[u] : s1[u]) : -INFINITY;
         }
       }
+      float t0 = s0[0], t1 = s1[0];
 #pragma unroll
-      for (int u = 0; u < 16; u++) {
+      for (int u = 1; u < 8; u++) {
         t0 = fmaxf(t0, s0[u]);
         t1 = fmaxf(t1, s1[u]);
       }
@@ -686,42 +725,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       t0 *= c2;
       t1 *= c2;
-      // the reference maximum moves only on rises above kLazy (the first rise
-      // from -inf finds an O of zeros: nothing to rescale)
-      const float n0 = t0 <= m0 + kLazy ? m0 : fmaxf(t0, m0), n1 = t1 <= m1 + kLazy ? m1 : fmaxf(t1, m1);
-      const float a0 = n0 == m0 || m0 == -INFINITY ? 1.f : exp2_approx(m0 - n0);
-      const float a1 = n1 == m1 || m1 == -INFINITY ? 1.f : exp2_approx(m1 - n1);
-      m0 = n0;
-      m1 = n1;
-      l0 *= a0;
-      l1 *= a1;
-      r0 *= a0;
-      r1 *= a1;
-      const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
-      if ((lane & 3) == 0) {
-        sm->alpha[stage][h0] = a0;
-        sm->alpha[stage][h1] = a1;
-      }
-      const uint32_t moved = bar_or(1, 32 * kSoftmaxWarps, a0 != 1.f || a1 != 1.f);
-      if (moved) ok = warp_wait(&sm->x_free[stage ^ 1], ((i - 1) >> 1) & 1) && ok;
-      if (moved && ok) {  // rescale O^T: lane = dim, columns = heads; the last second product is done
-        tc::tc_fence_after();
-#pragma unroll 1
-        for (int q = 0; q < 16; q++) {
-          const uint32_t ta = tmem + quarter + kOCol + 16 * q;
-          float v[16];
-          tc::tmem_ld16(ta, v);
-#pragma unroll
-          for (int h = 0; h < 16; h++) v[h] *= sm->alpha[stage][16 * (q & 3) + h];
-          tmem_st16(ta, v);
+      // the reference maximum moves only on rises above kLazy, in any head or half
+      if (bar_or(1, 32 * kSoftmaxWarps, fresh || t0 > m0 + kLazy || t1 > m1 + kLazy)) {
+        if ((lane & 3) == 0) {
+          sm->top[half][h0] = t0;
+          sm->top[half][h1] = t1;
         }
-        tmem_st_wait();
+        bar_or(1, 32 * kSoftmaxWarps, 0u);
+        t0 = fmaxf(t0, sm->top[half ^ 1][h0]);
+        t1 = fmaxf(t1, sm->top[half ^ 1][h1]);
+        const float n0 = t0 <= m0 + kLazy ? m0 : fmaxf(t0, m0), n1 = t1 <= m1 + kLazy ? m1 : fmaxf(t1, m1);
+        // (the first rise from -inf finds sums and an O of zeros)
+        const float a0 = n0 == m0 || m0 == -INFINITY ? 1.f : exp2_approx(m0 - n0);
+        const float a1 = n1 == m1 || m1 == -INFINITY ? 1.f : exp2_approx(m1 - n1);
+        m0 = n0;
+        m1 = n1;
+        l0 *= a0;
+        l1 *= a1;
+        r0 *= a0;
+        r1 *= a1;
+        if (!fresh) {  // rescale O^T (lane = dim, columns = heads), when the last second product is done
+          if (half == 0 && (lane & 3) == 0) {
+            sm->alpha[h0] = a0;
+            sm->alpha[h1] = a1;
+          }
+          bar_or(1, 32 * kSoftmaxWarps, 0u);
+          ok = warp_wait(&sm->x_free[stage ^ 1][1], ((i - 1) >> 1) & 1) && ok;
+          if (ok) {
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int q = half; q < 16; q += 2) {
+              const uint32_t ta = tmem + quarter + kOCol + 16 * q;
+              float v[16];
+              tc::tmem_ld16(ta, v);
+#pragma unroll
+              for (int h = 0; h < 16; h++) v[h] *= sm->alpha[16 * (q & 3) + h];
+              tmem_st16(ta, v);
+            }
+            tmem_st_wait();
+          }
+        }
       }
-      // P^T line `head`: 16-byte pieces of eight rows, swizzled with head & 7 (free once chunk i - 2 is done)
-      if (i >= 2) ok = warp_wait(&sm->x_free[stage], ((i >> 1) - 1) & 1) && ok;
+      fresh = false;
+      const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+      // P^T line `head`: 16-byte pieces of eight rows, swizzled with head & 7.  (The stage's P and S are
+      // free: this chunk's rows could only be stored when the product that read P(i - 2) was done.)
       uint8_t *p0 = sP + stage * kPBytes + h0 * 128 + 4 * (lane & 3), *p1 = p0 + 8 * 128;
 #pragma unroll
-      for (int u = 0; u < 8; u++) {
+      for (int u = 0; u < 4; u++) {
         const float x0 = exp2_approx(fmaf(s0[2 * u], c2, -b0)), x1 = exp2_approx(fmaf(s0[2 * u + 1], c2, -b0));
         const float y0 = exp2_approx(fmaf(s1[2 * u], c2, -b1)), y1 = exp2_approx(fmaf(s1[2 * u + 1], c2, -b1));
         l0 += x0 + x1;
@@ -730,19 +781,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t wx = *reinterpret_cast<const uint32_t *>(&px), wy = *reinterpret_cast<const uint32_t *>(&py);
         r0 += bf16x2_lo(wx) + bf16x2_hi(wx);
         r1 += bf16x2_lo(wy) + bf16x2_hi(wy);
-        *reinterpret_cast<uint32_t *>(p0 + ((u ^ (h0 & 7)) << 4)) = wx;
-        *reinterpret_cast<uint32_t *>(p1 + ((u ^ (h0 & 7)) << 4)) = wy;
+        const int at = ((4 * half + u) ^ (h0 & 7)) << 4;
+        *reinterpret_cast<uint32_t *>(p0 + at) = wx;
+        *reinterpret_cast<uint32_t *>(p1 + at) = wy;
       }
       tc::fence_proxy_async_smem();
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm->p_full[stage]);
+      look_ahead(i + 1);
 
       if (flags & kLast) {  // this CTA's part of the job is done
         const int32_t bt = job >> gs, g = job & ((1 << gs) - 1);
         const bool out_now = flags & kWhole;
-        ok = warp_wait(&sm->x_free[stage], (i >> 1) & 1) && ok;
-        tc::tc_fence_after();
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
           l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, o);
@@ -750,12 +801,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           r0 += __shfl_xor_sync(0xFFFFFFFFu, r0, o);
           r1 += __shfl_xor_sync(0xFFFFFFFFu, r1, o);
         }
+        const int h = (lane & 1) ? h1 : h0;  // lanes with lane % 4 < 2 look after a head each
+        float l = (lane & 1) ? l1 : l0, rounded = (lane & 1) ? r1 : r0;
+        const float m = (lane & 1) ? m1 : m0;
+        if ((lane & 3) < 2) {
+          sm->sums[half][h][0] = l;
+          sm->sums[half][h][1] = rounded;
+        }
+        bar_or(1, 32 * kSoftmaxWarps, 0u);
         const int heads = min(kH, a.H - g * kH);
         const int64_t out_row = static_cast<int64_t>(bt) * a.H + g * kH;
         const int64_t slot_o = 2 * static_cast<int64_t>(blockIdx.x) + (first_segment ? 0 : 1);
-        if ((lane & 3) < 2 && ok) {
-          const int h = (lane & 1) ? h1 : h0;
-          const float m = (lane & 1) ? m1 : m0, l = (lane & 1) ? l1 : l0, rounded = (lane & 1) ? r1 : r0;
+        if ((lane & 3) < 2 && half == 0 && ok) {
+          l += sm->sums[1][h][0];
+          rounded += sm->sums[1][h][1];
           if (out_now) {
             sm->l[h] = rounded == 0.f ? 0.f : 1.f / rounded;
             if (a.lse && h < heads) a.lse[out_row + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
@@ -764,54 +823,66 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         bar_or(1, 32 * kSoftmaxWarps, 0u);  // sm->l is in
+        ok = warp_wait(&sm->x_free[stage][1], (i >> 1) & 1) && ok;
+        if (ok) {
+          tc::tc_fence_after();
+          uint32_t next[16];
+          tmem_ld16_issue(tmem + quarter + kOCol + 16 * half, next);
 #pragma unroll 1
-        for (int q = 0; q < 16 && ok; q++) {  // 16 heads of a dim tile at a time
-          const int d = 128 * (q >> 2) + 32 * warp + lane, hb = 16 * (q & 3);
-          float v[16];
-          tc::tmem_ld16(tmem + quarter + kOCol + 16 * q, v);
-          if (out_now) {
-            // an 8 x 8 exchange among eight lanes: lane = dim, registers = heads, to a lane with eight dims of a head
-            uint32_t w1[8], w2[8], w3[8];
-            const uint32_t pick = (lane & 1) ? 0x3276u : 0x5410u;  // odd: other's high, own high half; even: own low, other's low
+          for (int q = half; q < 16; q += 2) {  // 16 heads of a dim tile at a time, the next ones on their way
+            const int d = 128 * (q >> 2) + 32 * (warp & 3) + lane, hb = 16 * (q & 3);
+            float v[16];
+            tc::tmem_ld_wait();
+            tmem_pin16(next);
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-              const __nv_bfloat162 two =
-                  __floats2bfloat162_rn(v[2 * k] * sm->l[hb + 2 * k], v[2 * k + 1] * sm->l[hb + 2 * k + 1]);
-              const uint32_t own = *reinterpret_cast<const uint32_t *>(&two);
-              w1[k] = __byte_perm(own, __shfl_xor_sync(0xFFFFFFFFu, own, 1), pick);  // head 2k + lane % 2
-            }
+            for (int k = 0; k < 16; k++) v[k] = __uint_as_float(next[k]);
+            if (q + 2 < 16) tmem_ld16_issue(tmem + quarter + kOCol + 16 * (q + 2), next);
+            if (out_now) {
+              // an 8 x 8 exchange among eight lanes: lane = dim, registers = heads, to a lane with eight dims of a head
+              uint32_t w1[8], w2[8], w3[8];
+              const uint32_t pick = (lane & 1) ? 0x3276u : 0x5410u;  // odd: other's high, own high half; even: own low, other's low
 #pragma unroll
-            for (int k = 0; k < 4; k++) {  // head 4k + lane % 4: words 2k, 2k + 1
-              const bool odd = lane & 2;
-              const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? w1[2 * k] : w1[2 * k + 1], 2);
-              w2[2 * k] = odd ? other : w1[2 * k];
-              w2[2 * k + 1] = odd ? w1[2 * k + 1] : other;
-            }
-            uint16_t *o = static_cast<uint16_t *>(a.out) + (out_row + hb + (lane & 7)) * kD + (d & ~7);
-#pragma unroll
-            for (int k = 0; k < 2; k++) {  // head 8k + lane % 8: words 4k .. 4k + 3
-              const bool odd = lane & 4;
-#pragma unroll
-              for (int j = 0; j < 2; j++) {
-                const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? w2[4 * k + j] : w2[4 * k + 2 + j], 4);
-                w3[4 * k + j] = odd ? other : w2[4 * k + j];
-                w3[4 * k + 2 + j] = odd ? w2[4 * k + 2 + j] : other;
+              for (int k = 0; k < 8; k++) {
+                const __nv_bfloat162 two =
+                    __floats2bfloat162_rn(v[2 * k] * sm->l[hb + 2 * k], v[2 * k + 1] * sm->l[hb + 2 * k + 1]);
+                const uint32_t own = *reinterpret_cast<const uint32_t *>(&two);
+                w1[k] = __byte_perm(own, __shfl_xor_sync(0xFFFFFFFFu, own, 1), pick);  // head 2k + lane % 2
               }
-              if (hb + 8 * k + (lane & 7) < heads)
-                *reinterpret_cast<uint4 *>(o + 8 * k * kD) = make_uint4(w3[4 * k], w3[4 * k + 1], w3[4 * k + 2], w3[4 * k + 3]);
-            }
-          } else {
-            float4 *o = ws.o + (slot_o * (kH / 4) + hb / 4) * kD + d;
 #pragma unroll
-            for (int k = 0; k < 4; k++) o[k * kD] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+              for (int k = 0; k < 4; k++) {  // head 4k + lane % 4: words 2k, 2k + 1
+                const bool odd = lane & 2;
+                const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? w1[2 * k] : w1[2 * k + 1], 2);
+                w2[2 * k] = odd ? other : w1[2 * k];
+                w2[2 * k + 1] = odd ? w1[2 * k + 1] : other;
+              }
+              uint16_t *o = static_cast<uint16_t *>(a.out) + (out_row + hb + (lane & 7)) * kD + (d & ~7);
+#pragma unroll
+              for (int k = 0; k < 2; k++) {  // head 8k + lane % 8: words 4k .. 4k + 3
+                const bool odd = lane & 4;
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                  const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? w2[4 * k + j] : w2[4 * k + 2 + j], 4);
+                  w3[4 * k + j] = odd ? other : w2[4 * k + j];
+                  w3[4 * k + 2 + j] = odd ? w2[4 * k + 2 + j] : other;
+                }
+                if (hb + 8 * k + (lane & 7) < heads)
+                  *reinterpret_cast<uint4 *>(o + 8 * k * kD) =
+                      make_uint4(w3[4 * k], w3[4 * k + 1], w3[4 * k + 2], w3[4 * k + 3]);
+              }
+            } else {
+              float4 *o = ws.o + (slot_o * (kH / 4) + hb / 4) * kD + d;
+#pragma unroll
+              for (int k = 0; k < 4; k++) o[k * kD] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
           }
+          tc::tc_fence_before();
         }
-        tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm->o_free);
         m0 = m1 = -INFINITY;
         l0 = l1 = r0 = r1 = 0.f;
         first_segment = false;
+        fresh = true;
       }
     }
   }
@@ -829,11 +900,14 @@ __device__ __forceinline__ float weight_of(float m, float M) { return m == M ? 1
 
 // Joins the partial results of jobs that span CTAs.  An item is such a job,
 // four of its heads and 32 or 128 of its dims (lane = dim).  First the partials'
-// weights are found, a thread for each partial, then the weighted sum runs
-// over the partials.  Where a job has few of them, as with many short jobs, a
-// warp joins an item by itself; where it has many, the eight warps of the CTA
-// take every eighth partial each and their sums meet in shared memory.
-__global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const lidx_paged_attn_args a, const Jobs jobs,
+// weights are found, a lane or a thread for each partial, then the weighted sum
+// runs over the partials, in their order.  Where a job has few of them, as with
+// many short jobs, a warp joins an item by itself; where it has many, the eight
+// warps of the CTA take every eighth partial each and their sums meet in shared
+// memory.  It is bound by the latency of a few dependent reads of L2, so what
+// helps is many of them in flight (112 registers): held to 80 registers for a third CTA on the
+// SM it took 1 to 2 us more.
+__global__ void __launch_bounds__(kMergeThreads, 2) paged_attn_merge_kernel(const lidx_paged_attn_args a, const Jobs jobs,
                                                                          const Scratch ws) {
   constexpr int kWarps = kMergeThreads / 32, kItems = (kH / 4) * (kD / 32);
   __shared__ Split list[kMaxCtas];  // jobs with few partials from the front, with many from the back
@@ -892,28 +966,35 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const l
     const Split sj = list[item / (kItems / 4)];
     const int h4 = (item % (kItems / 4)) / 4, d0 = 128 * (item % 4);
     const Deal deal(sj.total, jobs.G);
-    const int32_t from = deal.owner(sj.start), last = deal.owner(sj.end - 1);
-    float M[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, L[4] = {0.f, 0.f, 0.f, 0.f}, R[4] = {0.f, 0.f, 0.f, 0.f}, A[4][4] = {};
-#pragma unroll 1
-    for (int32_t c = from; c <= last; c++) {
-      look(ws.ml + slot_of(deal, c, sj.start) * kH + 4 * h4);
+    const int32_t from = deal.owner(sj.start), n = deal.owner(sj.end - 1) - from + 1;  // <= kFew
+    const int part = lane % kFew;  // the lane's partial
+    look(part < n ? ws.ml + slot_of(deal, from + part, sj.start) * kH + 4 * h4 : nullptr);
+    float M[4], L[4], R[4], A[4][4] = {};
 #pragma unroll
-      for (int k = 0; k < 4; k++) M[k] = fmaxf(M[k], m[k]);
+    for (int k = 0; k < 4; k++) {
+      M[k] = m[k];
+#pragma unroll
+      for (int o = 1; o < kFew; o <<= 1) M[k] = fmaxf(M[k], __shfl_xor_sync(0xFFFFFFFFu, M[k], o));
+      e[k] = part < n ? weight_of(m[k], M[k]) : 0.f;
+      L[k] = e[k] * l[k];
+      R[k] = e[k] * r[k];
+#pragma unroll
+      for (int o = 1; o < kFew; o <<= 1) {
+        L[k] += __shfl_xor_sync(0xFFFFFFFFu, L[k], o);
+        R[k] += __shfl_xor_sync(0xFFFFFFFFu, R[k], o);
+      }
     }
 #pragma unroll 2
-    for (int32_t c = from; c <= last; c++) {
-      const int32_t slot = slot_of(deal, c, sj.start);
-      look(ws.ml + slot * kH + 4 * h4);
+    for (int c = 0; c < n; c++) {
+      const float4 *o = ws.o + static_cast<size_t>(slot_of(deal, from + c, sj.start) * (kH / 4) + h4) * kD + d0 + lane;
       float4 v[4];
 #pragma unroll
-      for (int j = 0; j < 4; j++) v[j] = ws.o[static_cast<size_t>(slot * (kH / 4) + h4) * kD + d0 + 32 * j + lane];
+      for (int j = 0; j < 4; j++) v[j] = o[32 * j];
 #pragma unroll
       for (int k = 0; k < 4; k++) {
-        const float e0 = weight_of(m[k], M[k]);
-        L[k] = fmaf(e0, l[k], L[k]);
-        R[k] = fmaf(e0, r[k], R[k]);
+        const float w = __shfl_sync(0xFFFFFFFFu, e[k], c);
 #pragma unroll
-        for (int j = 0; j < 4; j++) A[k][j] = fmaf(e0, reinterpret_cast<const float *>(&v[j])[k], A[k][j]);
+        for (int j = 0; j < 4; j++) A[k][j] = fmaf(w, reinterpret_cast<const float *>(&v[j])[k], A[k][j]);
       }
     }
 #pragma unroll
@@ -951,14 +1032,24 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const l
     }
     __syncthreads();
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int32_t c = warp; c < n; c += kWarps) {
-      const float4 v = ws.o[static_cast<size_t>(slot_of(deal, from + c, sj.start) * (kH / 4) + h4) * kD + d0 + lane];
-      const float4 w = weight_s[c];
-      acc.x = fmaf(w.x, v.x, acc.x);
-      acc.y = fmaf(w.y, v.y, acc.y);
-      acc.z = fmaf(w.z, v.z, acc.z);
-      acc.w = fmaf(w.w, v.w, acc.w);
+#pragma unroll 1
+    for (int32_t c0 = warp; c0 < n; c0 += kBatch * kWarps) {
+      float4 v[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; u++) {
+        const int32_t c = c0 + u * kWarps;
+        v[u] = c < n ? ws.o[static_cast<size_t>(slot_of(deal, from + c, sj.start) * (kH / 4) + h4) * kD + d0 + lane]
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; u++) {
+        const float4 w = weight_s[min(c0 + u * kWarps, kMaxCtas - 1)];
+        const bool in = c0 + u * kWarps < n;
+        acc.x = fmaf(in ? w.x : 0.f, v[u].x, acc.x);
+        acc.y = fmaf(in ? w.y : 0.f, v[u].y, acc.y);
+        acc.z = fmaf(in ? w.z : 0.f, v[u].z, acc.z);
+        acc.w = fmaf(in ? w.w : 0.f, v[u].w, acc.w);
+      }
     }
     acc_s[warp][lane] = acc;
     __syncthreads();
@@ -1049,7 +1140,7 @@ cudaError_t launch_paged_attn(const lidx_paged_attn_args &a, void *ws, cudaStrea
     default: e = launch<LIDX_BF16>(tm, a, j, s, st); break;
   }
   if (e != cudaSuccess) return e;
-  return launch_kernel(paged_attn_merge_kernel, dim3(4 * sm_count()), dim3(kMergeThreads), 0, st, true, a, j, s);
+  return launch_kernel(paged_attn_merge_kernel, dim3(kMergeCtas * sm_count()), dim3(kMergeThreads), 0, st, true, a, j, s);
 }
 
 }  // namespace lidx
