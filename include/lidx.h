@@ -470,7 +470,8 @@ LIDX_API lidx_status lidx_paged_read(const lidx_paged_read_args *args, void *ws,
  *
  * for every block with rows, or, with `first`, those that hold a row >=
  * first[b] (the blocks that an append touched).  Summaries are kept by page,
- * as the rows are; the others stay as they were.  A block with a non-finite
+ * as the rows are; the others stay as they were.  Sequences that share
+ * a page share its summary, so they must hold the same rows of it.  A block with a non-finite
  * mean gets scale NaN and codes 0 (never selected by its score) and sets
  * LIDX_DEV_NAN; lens beyond the table are cut to it and set LIDX_DEV_BOUNDS.
  *   keys   dim 128: LIDX_F32 | LIDX_BF16 | LIDX_E4M3 | LIDX_E2M1

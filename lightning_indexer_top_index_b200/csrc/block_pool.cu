@@ -104,14 +104,14 @@ __device__ __forceinline__ bool sum_plane(const uint8_t *base, int64_t pitch, co
       if (r < count) {
         const uint8_t *src = base + (p0 + r) * pitch + piece * P::kBytes;
         if (P::kBytes == 16) {
-          w[i] = __ldg(reinterpret_cast<const uint4 *>(src));
+          w[i] = fetch(reinterpret_cast<const uint4 *>(src));
         } else {
-          const uint2 h = __ldg(reinterpret_cast<const uint2 *>(src));
+          const uint2 h = fetch(reinterpret_cast<const uint2 *>(src));
           w[i].x = h.x;
           w[i].y = h.y;
         }
-        if (kFmt == LIDX_E4M3) sc[i] = __ldg(scales + (p0 + r) * ld_scale);
-        if (kFmt == LIDX_E2M1) sc[i] = __ldg(scales + (p0 + r) * ld_scale + piece / 2);
+        if (kFmt == LIDX_E4M3) sc[i] = fetch(scales + (p0 + r) * ld_scale);
+        if (kFmt == LIDX_E2M1) sc[i] = fetch(scales + (p0 + r) * ld_scale + piece / 2);
       }
     }
 #pragma unroll
@@ -158,14 +158,14 @@ __global__ void __launch_bounds__(kThreads) block_pool_kernel(const lidx_block_p
   pdl_trigger();
   pdl_wait();
   bool cut;
-  const int32_t len = cut_len(__ldg(a.len + b), a.keys, cut);
+  const int32_t len = cut_len(fetch(a.len + b), a.keys, cut);
   if (cut && blockIdx.x == 0 && tid == 0) raise_status(status, LIDX_DEV_BOUNDS);
   const int32_t rows = a.keys.page_rows;
-  const int32_t first = a.first ? max(__ldg(a.first + b), 0) : 0;
+  const int32_t first = a.first ? max(fetch(a.first + b), 0) : 0;
   const int32_t nb = static_cast<int32_t>((static_cast<int64_t>(len) + rows - 1) >> shift);
   const lidx_kv &kv = a.keys.rows;
   for (int64_t j = (first >> shift) + static_cast<int64_t>(blockIdx.x); j < nb && first < len; j += gridDim.x) {
-    const int32_t page = __ldg(a.keys.table + static_cast<int64_t>(b) * a.keys.ld_table + j);
+    const int32_t page = fetch(a.keys.table + static_cast<int64_t>(b) * a.keys.ld_table + j);
     if (page < 0 || page >= a.keys.n_pages) {  // the same for the whole CTA
       if (tid == 0) raise_status(status, LIDX_DEV_BOUNDS);
       continue;

@@ -6,12 +6,21 @@
 
 namespace lidx {
 
+// A load of what the kernel before this one may have written (rows, tables,
+// lens, queries).  An ordinary one, which stays behind pdl_wait: a read-only
+// load (ld.global.nc) promises that nothing writes there while the kernel
+// runs, and a programmatic dependent launch runs before its predecessor ends.
+template <typename T>
+__device__ __forceinline__ T fetch(const T *p) {
+  return *p;
+}
+
 // Pool row of row r of sequence b, or -1 where the table has no page for it.
 // r >= 0; shift = log2(page_rows).
 __device__ __forceinline__ int32_t pool_row(const lidx_pages &c, int shift, int b, int32_t r) {
   const int32_t j = r >> shift;
   if (j >= c.max_pages) return -1;
-  const int32_t page = __ldg(c.table + static_cast<int64_t>(b) * c.ld_table + j);
+  const int32_t page = fetch(c.table + static_cast<int64_t>(b) * c.ld_table + j);
   if (page < 0 || page >= c.n_pages) return -1;
   return (page << shift) | (r & (c.page_rows - 1));
 }
@@ -100,22 +109,22 @@ struct Dims8 {
     codes = (kFmt == LIDX_E4M3 || kFmt == LIDX_E2M1) && d0 < q;
     if (kFmt == LIDX_F32) {
       const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const float *>(kv.data) + p * kv.ld + d0);
-      w[0] = __ldg(s);
-      w[kFmt == LIDX_F32] = __ldg(s + 1);
+      w[0] = fetch(s);
+      w[kFmt == LIDX_F32] = fetch(s + 1);
     } else if (!codes) {
       const uint16_t *s = kFmt == LIDX_BF16 ? static_cast<const uint16_t *>(kv.data) + p * kv.ld + d0
                                             : static_cast<const uint16_t *>(kv.rope) + p * kv.ld_rope + (d0 - q);
-      w[0] = __ldg(reinterpret_cast<const uint4 *>(s));
+      w[0] = fetch(reinterpret_cast<const uint4 *>(s));
     } else {
       const uint8_t *data = static_cast<const uint8_t *>(kv.data) + p * kv.ld;
       if (kFmt == LIDX_E4M3) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(data + d0));
+        const uint2 x = fetch(reinterpret_cast<const uint2 *>(data + d0));
         w[0].x = x.x;
         w[0].y = x.y;
       } else {
-        w[0].x = __ldg(reinterpret_cast<const uint32_t *>(data + d0 / 2));
+        w[0].x = fetch(reinterpret_cast<const uint32_t *>(data + d0 / 2));
       }
-      scale = __ldg(kv.scale + p * kv.ld_scale + d0 / (kFmt == LIDX_E4M3 ? 64 : 32));
+      scale = fetch(kv.scale + p * kv.ld_scale + d0 / (kFmt == LIDX_E4M3 ? 64 : 32));
     }
   }
 

@@ -27,14 +27,14 @@ __device__ __forceinline__ void load16(const void *x, int dtype, int64_t at, flo
     const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(x) + at);
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      const float4 a = __ldg(s + i);
+      const float4 a = fetch(s + i);
       v[4 * i] = a.x; v[4 * i + 1] = a.y; v[4 * i + 2] = a.z; v[4 * i + 3] = a.w;
     }
   } else {
     const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + at);
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-      const uint4 a = __ldg(s + i);
+      const uint4 a = fetch(s + i);
       const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
       for (int k = 0; k < 4; k++) {
@@ -63,14 +63,14 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const lidx_paged
 #pragma unroll
   for (int k = 0; k < 16; k++) x[k] = 0.f;
   if (i < a.n) {
-    seq = __ldg(a.seq + i);
-    row = __ldg(a.row + i);
-    if (a.inv_freq) pos = a.pos ? __ldg(a.pos + i) : row;
+    seq = fetch(a.seq + i);
+    row = fetch(a.row + i);
+    if (a.inv_freq) pos = a.pos ? fetch(a.pos + i) : row;
     load16(a.x, a.x_dtype, i * a.ld_x + 16 * t, x);
   }
   if (a.inv_freq) {
 #pragma unroll
-    for (int k = 0; k < kAngles; k++) freq[k] = __ldg(a.inv_freq + t * kAngles + k);
+    for (int k = 0; k < kAngles; k++) freq[k] = fetch(a.inv_freq + t * kAngles + k);
   }
   int32_t dst = -1;
   if (seq >= 0) {
@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(kThreads) paged_read_kernel(const lidx_paged_r
   Dims8<kFmt> raw[kPer];
 #pragma unroll
   for (int r = 0; r < kPer; r++) {
-    seq[r] = i0 + r < a.n ? __ldg(a.seq + i0 + r) : -1;
-    row[r] = i0 + r < a.n ? __ldg(a.row + i0 + r) : -1;
+    seq[r] = i0 + r < a.n ? fetch(a.seq + i0 + r) : -1;
+    row[r] = i0 + r < a.n ? fetch(a.row + i0 + r) : -1;
   }
 #pragma unroll
   for (int r = 0; r < kPer; r++)

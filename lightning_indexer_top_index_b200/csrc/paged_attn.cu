@@ -146,9 +146,9 @@ struct Deal {
 // Entries of job's row list: rows for the dense case, rows of the listed blocks otherwise.
 __device__ __forceinline__ int32_t job_rows(const lidx_paged_attn_args &a, int32_t job, int gs, int shift) {
   const int32_t bt = job >> gs;
-  if (a.blocks) return (a.n_sel ? min(max(__ldg(a.n_sel + bt), 0), a.n_blocks) : a.n_blocks) << shift;
+  if (a.blocks) return (a.n_sel ? min(max(fetch(a.n_sel + bt), 0), a.n_blocks) : a.n_blocks) << shift;
   bool cut;
-  return max(cut_len(__ldg(a.len + bt / a.T), a.cache, cut) - (a.T - 1 - bt % a.T), 0);
+  return max(cut_len(fetch(a.len + bt / a.T), a.cache, cut) - (a.T - 1 - bt % a.T), 0);
 }
 __device__ __forceinline__ int32_t job_chunks(const lidx_paged_attn_args &a, int32_t job, int gs, int shift) {
   return (job_rows(a, job, gs, shift) + kRows - 1) / kRows;
@@ -301,7 +301,7 @@ __device__ __forceinline__ int32_t entry_row(const lidx_paged_attn_args &a, int3
   if (e >= n_list) return -1;
   int32_t r = e, b = bt / a.T;
   if (a.blocks) {
-    const int32_t j = __ldg(a.blocks + static_cast<int64_t>(bt) * a.ld_blocks + (e >> shift));
+    const int32_t j = fetch(a.blocks + static_cast<int64_t>(bt) * a.ld_blocks + (e >> shift));
     if (j < 0 || j >= a.cache.max_pages) {
       bounds |= j != -1;
       return -1;
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         left = (rows + kRows - 1) / kRows - c;
         const int32_t bt = job >> gs;
         bool cut;
-        seen = cut_len(__ldg(a.len + bt / a.T), a.cache, cut) - (a.T - 1 - bt % a.T);
+        seen = cut_len(fetch(a.len + bt / a.T), a.cache, cut) - (a.T - 1 - bt % a.T);
         bounds |= cut;
         whole = c == 0;
         flags = kFirst;
@@ -520,15 +520,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             v[q][it] = make_uint4(0, 0, 0, 0);
             sc[q][it] = 127u;
             if (row[it] >= 0 && (q < 3 || in_last)) {
-              v[q][it] = __ldg(reinterpret_cast<const uint4 *>(data + row[it] * pitch + q * (F::kPieces * 16)));
-              if (kQuant) sc[q][it] = __ldg(scales + row[it] * kv.ld_scale + q * (kFmt == LIDX_E2M1 ? 4 : 2));
+              v[q][it] = fetch(reinterpret_cast<const uint4 *>(data + row[it] * pitch + q * (F::kPieces * 16)));
+              if (kQuant) sc[q][it] = fetch(scales + row[it] * kv.ld_scale + q * (kFmt == LIDX_E2M1 ? 4 : 2));
             }
           }
           if (kQuant && q == 3) {
 #pragma unroll
             for (int it = 0; it < 2; it++) {
               rv[it] = make_uint4(0, 0, 0, 0);
-              if (rope_row[it] >= 0) rv[it] = __ldg(reinterpret_cast<const uint4 *>(rope + rope_row[it] * 2 * kv.ld_rope));
+              if (rope_row[it] >= 0) rv[it] = fetch(reinterpret_cast<const uint4 *>(rope + rope_row[it] * (2 * kv.ld_rope)));
             }
           }
         }
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = tid; i < heads * kD / 8; i += 32 * kSoftmaxWarps) o[i] = make_uint4(0, 0, 0, 0);
       if (a.lse && tid < heads) a.lse[row + tid] = -INFINITY;
       bool cut;
-      cut_len(__ldg(a.len + bt / a.T), a.cache, cut);
+      cut_len(fetch(a.len + bt / a.T), a.cache, cut);
       if (cut && tid == 0) raise_status(ws.status, LIDX_DEV_BOUNDS);
     }
     const int half = warp >> 2, h0 = (warp & 3) * 16 + (lane >> 2), h1 = h0 + 8;  // this lane's heads
