@@ -254,6 +254,62 @@ def test_pool_hard_values(cuda_device):
         assert scale[p].item() == ws or (np.isnan(ws) and np.isnan(scale[p].item())), p
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1", "bf16", "f32"])
+@pytest.mark.parametrize("P", [16, 64, 256])
+def test_pool_long_tables(cuda_device, fmt, P):
+    """Tables with room for many blocks (a warp sums one by itself), most of them not there yet."""
+    g = np.random.default_rng(40 + P)
+    lens = [5 * P + 1, 0, 1, P, 2 * P - 1, 37 * P - 3]
+    table, n_pages = _table(g, lens, P)
+    wide = np.full((len(lens), 500), -1, np.int32)
+    wide[:, :table.shape[1]] = table
+    c = _cache(g, fmt, 128, n_pages, P, wide, pad=1)
+    codes = torch.full((n_pages, 128), 55, dtype=torch.int8, device=DEV)
+    scale = torch.full((n_pages,), 7.0, device=DEV)
+    if fmt != "f32":  # a block of zeros
+        for plane in (t for t in (c.rows.data, c.rows.scale, c.rows.rope) if t is not None):
+            plane.view(n_pages, P, -1)[int(table[5, 3])] = 0
+    else:  # ... and sums that cancel, subnormals, a NaN
+        d = c.rows.data.view(n_pages, P, -1)
+        d[int(table[5, 3])] = 0.0
+        d[int(table[5, 4])] = torch.from_numpy((g.standard_normal((P, d.shape[2])) * 1e-41).astype(np.float32)).to(DEV)
+        d[int(table[5, 5]), 0::2] = 3e38
+        d[int(table[5, 5]), 1::2] = -3e38
+        d[int(table[5, 5]), 0, 5] = 1.0
+        d[int(table[5, 6]), P - 1, 100] = float("nan")
+    call = L.block_pool_call(c, _i32(lens), codes, scale)
+    call()
+    assert call.status() == (L.DEV_NAN if fmt == "f32" else 0)
+    want = ref.pool(_values(c, fmt), wide, P, n_pages, lens)
+    for p in range(n_pages):
+        wc, ws = want.get(p, (np.full(128, 55, np.int8), np.float32(7.0)))
+        assert np.array_equal(codes[p].cpu().numpy(), wc), p
+        assert scale[p].item() == ws or (np.isnan(ws) and np.isnan(scale[p].item())), p
+
+
+def test_pool_borders(cuda_device):
+    """Means on and next to the middle between two codes, and quotients next to a border of fp32."""
+    g = np.random.default_rng(47)
+    P, n_pages = 16, 2400
+    table = np.arange(n_pages, dtype=np.int32)[None]
+    c = _cache(g, "f32", 128, n_pages, P, table)
+    x = np.rint(g.uniform(-127, 127, (n_pages, 128)) * 2) / 2  # whole and half codes of a largest mean of 127
+    x[:, 7] = 127.0
+    x = x.astype(np.float32)
+    half = n_pages // 2
+    x[half:] = np.nextafter(x[half:], (np.where(g.random((n_pages - half, 128)) < 0.5, -1e9, 1e9)).astype(np.float32))
+    x *= (2.0 ** g.integers(-140, 100, (n_pages, 1))).astype(np.float32)
+    c.rows.data[:, :128] = torch.from_numpy(np.repeat(x, P, axis=0)).to(DEV)
+    codes = torch.zeros((n_pages, 128), dtype=torch.int8, device=DEV)
+    scale = torch.zeros(n_pages, device=DEV)
+    call = L.block_pool_call(c, _i32([n_pages * P]), codes, scale)
+    call()
+    assert call.status() == 0
+    want = ref.pool(_values(c, "f32"), table, P, n_pages, [n_pages * P])
+    assert np.array_equal(codes.cpu().numpy(), np.stack([want[p][0] for p in range(n_pages)]))
+    assert np.array_equal(scale.cpu().numpy(), np.array([want[p][1] for p in range(n_pages)], np.float32))
+
+
 # ------------------------------------------------------------------ select
 def _summaries(g, n_pages):
     codes = np.clip(np.rint(g.standard_normal((n_pages, 128)) * 40), -127, 127).astype(np.int8)
