@@ -4,11 +4,12 @@
 // pos * inv_freq[i], the others rounded to E4M3 or E2M1 under one power-of-two
 // scale per 64 or 32 of them, and the row goes to its page.
 //
-// A row is served by dim/16 lanes, lane t holding dims [16t, 16t + 16): a
-// whole warp for a 512-wide row, eight lanes for an index key.  The row's 32
-// angles are spread over its lanes (one, or four, each) and fetched by
-// shuffles by the four lanes that hold the rotated dims, so no lane evaluates
-// more than its share of sines.  An angle is formed as pos * inv_freq / 2 pi
+// A row is served by a warp, or by eight lanes for an index key.  A lane has a
+// share of the dims that are rounded (16 of 28 lanes, or 8 of eight) and, of the
+// rotated ones, the pairs whose angles it evaluates (one, or four), so that no
+// value or angle is handed from lane to lane: with the rotated dims held 16 a
+// lane by four lanes and their angles fetched by shuffles, 20011 rows of 512,
+// appended and read back, took 28.4 us instead of 25.6.  An angle is formed as pos * inv_freq / 2 pi
 // turns in 64 bits and its whole turns dropped before it is rounded to fp32
 // (error below 2^-25 turns at any position), since in fp32 the product alone
 // would be off by up to pos * 2^-24 radians.
@@ -19,58 +20,120 @@ namespace lidx {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
-__device__ __forceinline__ void load16(const void *x, int dtype, int64_t at, float (&v)[16]) {
+// N adjacent values, at a multiple of N of a row (of 4, 2 or 1 for smaller ones).
+template <int N>
+__device__ __forceinline__ void load_values(const void *x, int dtype, int64_t at, float *v) {
   if (dtype == LIDX_F32) {
-    const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(x) + at);
+    const float *s = static_cast<const float *>(x) + at;
+    if constexpr (N % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const float4 a = fetch(s + i);
-      v[4 * i] = a.x; v[4 * i + 1] = a.y; v[4 * i + 2] = a.z; v[4 * i + 3] = a.w;
+      for (int i = 0; i < N / 4; i++) {
+        const float4 a = fetch(reinterpret_cast<const float4 *>(s) + i);
+        v[4 * i] = a.x; v[4 * i + 1] = a.y; v[4 * i + 2] = a.z; v[4 * i + 3] = a.w;
+      }
+    } else if constexpr (N == 2) {
+      const float2 a = fetch(reinterpret_cast<const float2 *>(s));
+      v[0] = a.x; v[1] = a.y;
+    } else {
+      v[0] = fetch(s);
     }
   } else {
-    const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + at);
+    const uint16_t *s = static_cast<const uint16_t *>(x) + at;
+    if constexpr (N % 8 == 0) {
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-      const uint4 a = fetch(s + i);
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+      for (int i = 0; i < N / 8; i++) {
+        const uint4 a = fetch(reinterpret_cast<const uint4 *>(s) + i);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
-        v[8 * i + 2 * k] = bf16x2_lo(w[k]);
-        v[8 * i + 2 * k + 1] = bf16x2_hi(w[k]);
+        for (int k = 0; k < 4; k++) {
+          v[8 * i + 2 * k] = bf16x2_lo(w[k]);
+          v[8 * i + 2 * k + 1] = bf16x2_hi(w[k]);
+        }
       }
+    } else if constexpr (N == 4) {
+      const uint2 a = fetch(reinterpret_cast<const uint2 *>(s));
+      v[0] = bf16x2_lo(a.x); v[1] = bf16x2_hi(a.x); v[2] = bf16x2_lo(a.y); v[3] = bf16x2_hi(a.y);
+    } else if constexpr (N == 2) {
+      const uint32_t a = fetch(reinterpret_cast<const uint32_t *>(s));
+      v[0] = bf16x2_lo(a); v[1] = bf16x2_hi(a);
+    } else {
+      v[0] = bf16x2_lo(fetch(s));
     }
   }
 }
 
+template <int N>
+__device__ __forceinline__ void store_f32(float *o, const float *v) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; i++)
+      reinterpret_cast<float4 *>(o)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else if constexpr (N == 2) {
+    *reinterpret_cast<float2 *>(o) = make_float2(v[0], v[1]);
+  } else {
+    o[0] = v[0];
+  }
+}
+
+// `odd`: some may be NaN
+template <int N>
+__device__ __forceinline__ void store_bf16(uint16_t *o, const float *v, bool odd) {
+  if constexpr (N % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 8; i++)
+      reinterpret_cast<uint4 *>(o)[i] = odd ? pack8_bf16(v + 8 * i) : pack8_bf16_numbers(v + 8 * i);
+  } else if constexpr (N == 1) {
+    o[0] = static_cast<uint16_t>(bf16_bits(v[0]));
+  } else {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; i++) w[i] = bf16_bits(v[2 * i]) | (bf16_bits(v[2 * i + 1]) << 16);
+    if constexpr (N == 4) *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t *>(o) = w[0];
+  }
+}
+
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
 template <int kDim>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const lidx_paged_append_args a, int shift,
                                                                  uint32_t *status) {
-  constexpr int kLanes = kDim / 16;          // lanes of a row
-  constexpr int kAngles = 32 / kLanes;       // angles a lane evaluates
-  const int t = threadIdx.x % kLanes, lane = threadIdx.x & 31;
-  const int base = lane - t;                 // the row's first lane
+  constexpr int kLanes = kDim / 16;            // lanes of a row
+  constexpr int kPairs = 32 / kLanes;          // pairs, and angles, of a lane
+  constexpr int kN = kDim == 512 ? 16 : 8;     // a lane's other dims
+  constexpr int kHolders = (kDim - 64) / kN;   // lanes that have some
+  const int t = threadIdx.x % kLanes;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / kLanes) + threadIdx.x / kLanes;
-  const int rl = t - (kLanes - 4);  // >= 0: lane rl of the four that hold the 64 RoPE dims
-  float freq[kAngles];
+  const bool holds = t < kHolders, adjacent = a.rope_pairs == LIDX_ROPE_ADJACENT;
+  // the lane's pairs: their first values from dim u0, and, by halves, their second ones from dim u0 + 32
+  const int u0 = kDim - 64 + (adjacent ? 2 : 1) * kPairs * t;
   pdl_trigger();
   pdl_wait();  // rows, positions and tables may come from the previous kernel
   // lanes of rows behind the last one stay for the shuffles
   int seq = -1, row = -1, pos = 0;
-  float x[16];
+  float x[kN], r[2 * kPairs], freq[kPairs];  // r: as stored, (u, v) pairs or the u's and then the v's
 #pragma unroll
-  for (int k = 0; k < 16; k++) x[k] = 0.f;
+  for (int k = 0; k < kN; k++) x[k] = 0.f;
+#pragma unroll
+  for (int k = 0; k < 2 * kPairs; k++) r[k] = 0.f;
   if (i < a.n) {
     seq = fetch(a.seq + i);
     row = fetch(a.row + i);
     if (a.inv_freq) pos = a.pos ? fetch(a.pos + i) : row;
-    load16(a.x, a.x_dtype, i * a.ld_x + 16 * t, x);
+    if (holds) load_values<kN>(a.x, a.x_dtype, i * a.ld_x + kN * t, x);
+    if (adjacent) {
+      load_values<2 * kPairs>(a.x, a.x_dtype, i * a.ld_x + u0, r);
+    } else {
+      load_values<kPairs>(a.x, a.x_dtype, i * a.ld_x + u0, r);
+      load_values<kPairs>(a.x, a.x_dtype, i * a.ld_x + u0 + 32, r + kPairs);
+    }
   }
   if (a.inv_freq) {
 #pragma unroll
-    for (int k = 0; k < kAngles; k++) freq[k] = fetch(a.inv_freq + t * kAngles + k);
+    for (int k = 0; k < kPairs; k++) freq[k] = fetch(a.inv_freq + t * kPairs + k);
   }
   int32_t dst = -1;
   if (seq >= 0) {
@@ -78,52 +141,37 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const lidx_paged
     if (dst < 0 && t == 0) raise_status(status, LIDX_DEV_BOUNDS);
   }
   // the largest magnitude by its bits; infinities and NaNs have the largest
-  uint32_t top = 0u;
+  uint32_t top = 0u, top_r = 0u;
 #pragma unroll
-  for (int k = 0; k < 16; k++) top = max(top, __float_as_uint(x[k]) & 0x7FFFFFFFu);
-  const bool nonfinite = top >= 0x7F800000u;
+  for (int k = 0; k < kN; k++) top = max(top, magnitude(x[k]));
+#pragma unroll
+  for (int k = 0; k < 2 * kPairs; k++) top_r = max(top_r, magnitude(r[k]));
+  const bool nonfinite = max(top, top_r) >= 0x7F800000u;
   if (nonfinite && dst >= 0) raise_status(status, LIDX_DEV_NAN);
   const bool odd = __any_sync(kAll, nonfinite);  // the warp's rows take the careful way
   if (odd) {
     top = 0u;
 #pragma unroll
-    for (int k = 0; k < 16; k++) top = isfinite(x[k]) ? max(top, __float_as_uint(x[k]) & 0x7FFFFFFFu) : top;
+    for (int k = 0; k < kN; k++) top = isfinite(x[k]) ? max(top, magnitude(x[k])) : top;
   }
-  // ... of the block: two or four neighbouring lanes
+  // ... of the block: the lanes that hold its 64 or 32 dims
   const int dtype = a.cache.rows.dtype;
-  top = max(top, __shfl_xor_sync(kAll, top, 1));
-  if (dtype == LIDX_E4M3) top = max(top, __shfl_xor_sync(kAll, top, 2));
+  constexpr int kShare = 32 / kN;  // lanes of 32 dims
+#pragma unroll
+  for (int o = 1; o < kShare; o <<= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+  if (dtype == LIDX_E4M3) top = max(top, __shfl_xor_sync(kAll, top, kShare));
 
   if (a.inv_freq) {
-    float cs[kAngles], sn[kAngles];
 #pragma unroll
-    for (int k = 0; k < kAngles; k++) {
+    for (int k = 0; k < kPairs; k++) {
       double turns = static_cast<double>(pos) * static_cast<double>(freq[k]) * 0.15915494309189533577;
       turns -= rint(turns);
-      sincospif(2.f * static_cast<float>(turns), &sn[k], &cs[k]);
-    }
-    const int from = rl < 0 ? 0 : rl;
-    if (a.rope_pairs == LIDX_ROPE_ADJACENT) {  // lane rl holds pairs 8 rl .. 8 rl + 7
-#pragma unroll
-      for (int k = 0; k < 8; k++) {
-        // pair 8 rl + k: angle slot (8 rl + k) % kAngles of lane (8 rl + k) / kAngles
-        const int src = base + (8 * from + k) / kAngles;
-        const float c = __shfl_sync(kAll, cs[k % kAngles], src), s = __shfl_sync(kAll, sn[k % kAngles], src);
-        if (rl >= 0) {
-          const float p = x[2 * k], q = x[2 * k + 1];
-          x[2 * k] = fmaf(p, c, -(q * s));
-          x[2 * k + 1] = fmaf(p, s, q * c);
-        }
-      }
-    } else {  // lanes 0, 1 hold the first halves of the pairs 16 (rl & 1) .. + 15, lanes 2, 3 their second halves
-#pragma unroll
-      for (int k = 0; k < 16; k++) {
-        const int src = base + (16 * (from & 1) + k) / kAngles;
-        const float c = __shfl_sync(kAll, cs[k % kAngles], src);
-        const float s = __shfl_sync(kAll, sn[k % kAngles], src);
-        const float o = __shfl_xor_sync(kAll, x[k], 2);
-        if (rl >= 0) x[k] = rl < 2 ? fmaf(x[k], c, -(o * s)) : fmaf(o, s, x[k] * c);
-      }
+      float s, c;
+      sincospif(2.f * static_cast<float>(turns), &s, &c);
+      float &u = r[adjacent ? 2 * k : k], &v = r[adjacent ? 2 * k + 1 : kPairs + k];
+      const float p = u, q = v;
+      u = fmaf(p, c, -(q * s));
+      v = fmaf(p, s, q * c);
     }
   }
 
@@ -131,36 +179,52 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const lidx_paged
 
   const lidx_kv &kv = a.cache.rows;
   const int64_t p = dst;
+  // the rotated dims
   if (dtype == LIDX_F32) {
-    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(const_cast<void *>(kv.data)) + p * kv.ld + 16 * t);
-#pragma unroll
-    for (int k = 0; k < 4; k++) o[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-  } else if (dtype == LIDX_BF16 || rl >= 0) {
-    uint16_t *o = dtype == LIDX_BF16 ? static_cast<uint16_t *>(const_cast<void *>(kv.data)) + p * kv.ld + 16 * t
-                                     : static_cast<uint16_t *>(const_cast<void *>(kv.rope)) + p * kv.ld_rope + 16 * rl;
-    reinterpret_cast<uint4 *>(o)[0] = odd ? pack8_bf16(x) : pack8_bf16_numbers(x);
-    reinterpret_cast<uint4 *>(o)[1] = odd ? pack8_bf16(x + 8) : pack8_bf16_numbers(x + 8);
-  } else {
-    const bool e4m3 = dtype == LIDX_E4M3;
-    const float am = __uint_as_float(top);
-    const int e = top ? (e4m3 ? block_exponent_e4m3(am) : block_exponent_e2m1(am)) : 0;
-    const float inv = inverse_scale(e);
-#pragma unroll
-    for (int k = 0; k < 16; k++) x[k] *= inv;
-    uint8_t *data = static_cast<uint8_t *>(const_cast<void *>(kv.data)) + p * kv.ld;
-    uint8_t *scale = const_cast<uint8_t *>(kv.scale) + p * kv.ld_scale;
-    if (e4m3) {
-      *reinterpret_cast<uint4 *>(data + 16 * t) =
-          odd ? make_uint4(pack4_e4m3(x), pack4_e4m3(x + 4), pack4_e4m3(x + 8), pack4_e4m3(x + 12))
-              : make_uint4(pack4_e4m3_in_range(x), pack4_e4m3_in_range(x + 4), pack4_e4m3_in_range(x + 8),
-                           pack4_e4m3_in_range(x + 12));
-      if ((t & 3) == 0) scale[t / 4] = static_cast<uint8_t>(e + 127);
+    float *o = static_cast<float *>(const_cast<void *>(kv.data)) + p * kv.ld;
+    if (adjacent) {
+      store_f32<2 * kPairs>(o + u0, r);
     } else {
-      *reinterpret_cast<uint2 *>(data + 8 * t) = 
-          odd ? make_uint2(pack8_e2m1(x), pack8_e2m1(x + 8))
-              : make_uint2(pack8_e2m1_finite(x), pack8_e2m1_finite(x + 8));
-      if ((t & 1) == 0) scale[t / 2] = static_cast<uint8_t>(e + 127);
+      store_f32<kPairs>(o + u0, r);
+      store_f32<kPairs>(o + u0 + 32, r + kPairs);
     }
+    if (holds) store_f32<kN>(o + kN * t, x);
+    return;
+  }
+  uint16_t *o = dtype == LIDX_BF16 ? static_cast<uint16_t *>(const_cast<void *>(kv.data)) + p * kv.ld
+                                   : static_cast<uint16_t *>(const_cast<void *>(kv.rope)) + p * kv.ld_rope - (kDim - 64);
+  if (adjacent) {
+    store_bf16<2 * kPairs>(o + u0, r, odd);
+  } else {
+    store_bf16<kPairs>(o + u0, r, odd);
+    store_bf16<kPairs>(o + u0 + 32, r + kPairs, odd);
+  }
+  if (!holds) return;
+  if (dtype == LIDX_BF16) {
+    store_bf16<kN>(o + kN * t, x, odd);
+    return;
+  }
+  const bool e4m3 = dtype == LIDX_E4M3;
+  const float am = __uint_as_float(top);
+  const int e = top ? (e4m3 ? block_exponent_e4m3(am) : block_exponent_e2m1(am)) : 0;
+  const float inv = inverse_scale(e);
+#pragma unroll
+  for (int k = 0; k < kN; k++) x[k] *= inv;
+  uint8_t *data = static_cast<uint8_t *>(const_cast<void *>(kv.data)) + p * kv.ld;
+  uint8_t *scale = const_cast<uint8_t *>(kv.scale) + p * kv.ld_scale;
+  uint32_t w[kN / 4];
+  if (e4m3) {
+#pragma unroll
+    for (int k = 0; k < kN / 4; k++) w[k] = odd ? pack4_e4m3(x + 4 * k) : pack4_e4m3_in_range(x + 4 * k);
+    if constexpr (kN == 16) *reinterpret_cast<uint4 *>(data + 16 * t) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *reinterpret_cast<uint2 *>(data + 8 * t) = make_uint2(w[0], w[1]);
+    if (t % (2 * kShare) == 0) scale[t / (2 * kShare)] = static_cast<uint8_t>(e + 127);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kN / 8; k++) w[k] = odd ? pack8_e2m1(x + 8 * k) : pack8_e2m1_finite(x + 8 * k);
+    if constexpr (kN == 16) *reinterpret_cast<uint2 *>(data + 8 * t) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t *>(data + 4 * t) = w[0];
+    if (t % kShare == 0) scale[t / kShare] = static_cast<uint8_t>(e + 127);
   }
 }
 
