@@ -678,7 +678,8 @@ LIDX_API lidx_status lidx_workspace_size(int op, const void *args, size_t *bytes
  * scorer, the decode layer and the append; 1 for lidx_topk_select on rows
  * one cluster holds, 4 beyond (segment selects, candidate gather, candidate
  * select, map back); 2 for lidx_sparse_attn_decode (split kernel, merge);
- * for lidx_selection_eval the sum over the requested ops.  Memsets and
+ * for lidx_selection_eval the sum over the requested ops; 1 for the calls on
+ * paged caches, 2 for lidx_paged_attn (attention, merge).  Memsets and
  * copies a call enqueues are not counted.  For launch accounting and for
  * checking a captured graph. */
 LIDX_API lidx_status lidx_launch_count(int op, const void *args, int *count);
