@@ -64,12 +64,14 @@ __device__ __forceinline__ void e2m1x8_to_bf16x2(uint32_t w, uint32_t (&o)[4]) {
 }
 
 // Eight E2M1 codes times their block's scale 2^(c - 127) as four bf16 pairs,
-// exactly, with half of the work on the multiply pipe (the byte permutes above
-// all run on the integer pipe, which bounds the attention's loader).  The
-// three magnitude bits of a code, put at bits 8..6 of a bf16, are its value
-// times 2^-126 (0.5 is a bf16 subnormal there), so one product with
-// 2^(126 + e) decodes and scales.  B * (2^6 + 2^18) puts a byte's two codes in
-// place in the two halves; scales above 2 take a second product.
+// exactly.  The three magnitude bits of a code, put at bits 8..6 of a bf16, are
+// its value times 2^-126 (0.5 is a bf16 subnormal there), so one product with
+// 2^(126 + e) decodes and scales; scales above 2 take a second one.  A byte's two
+// codes come to the two halves by a permute (their upper bytes by its sign mode,
+// which gives zeros here), one product with 2^6 + 2^12 puts magnitude and sign
+// bits in place, and a mask leaves only those: 19 instructions for eight values,
+// half of them on the multiply pipe (the lookup above all runs on the integer
+// pipe, which bounds the attention's loader).
 struct E2m1Scale {
   uint32_t s1, s2;
   bool two;  // the same in all lanes of a converged warp
@@ -81,10 +83,12 @@ struct E2m1Scale {
     two = __any_sync(0xFFFFFFFFu, c > 128u);
   }
   __device__ __forceinline__ void expand(uint32_t w, uint32_t (&o)[4]) const {
+    const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      const uint32_t x = ((w >> (8 * i)) & 0xFFu) * 0x00040040u;
-      o[i] = mul_bf16x2(((x * 64u) & 0x80008000u) | (x & 0x01C001C0u), s1);
+      uint32_t y;
+      asm("prmt.b32 %0, %1, %2, %3;" : "=r"(y) : "r"(even), "r"(odd), "r"(0xC480u + 0x1111u * i));
+      o[i] = mul_bf16x2((y * 0x1040u) & 0x81C081C0u, s1);
     }
     if (two) {
 #pragma unroll

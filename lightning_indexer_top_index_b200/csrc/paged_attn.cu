@@ -177,7 +177,9 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatil
   return false;
 }
 
-// A whole warp waits: the same answer in all lanes.
+// A whole warp waits: the same answer in all lanes.  (With lane 0 waiting and a
+// shuffle of its answer, each hand-over between the roles was 100 cycles longer:
+// 100 against 90 us for 256 queries of 1024 rows.)
 __device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, volatile uint32_t *abort) {
   return __all_sync(0xFFFFFFFFu, wait_for(bar, parity, abort));
 }
@@ -397,13 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
   const int n = my1 - my0;  // this CTA's chunks
-  auto warp_wait = [&](uint64_t *bar, uint32_t parity) {  // lane 0 waits; its view becomes the warp's
-    bool in = true;
-    if (lane == 0) in = wait_for(bar, parity, abort_flag);
-    in = __shfl_sync(0xFFFFFFFFu, in, 0);
-    __syncwarp();
-    return in;
-  };
+  auto warp_wait = [&](uint64_t *bar, uint32_t parity) { return wait_all(bar, parity, abort_flag); };
 
   if (warp == kScout) {
     // -------------------------------------------------------------- scout
