@@ -664,8 +664,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool fresh = true;          // nothing of the job is in O yet
     uint32_t next_valid = 0u, next_flags = 0u;  // what the scout says about the next chunk
     int32_t next_job = 0;
-    // After a wait that gave up the warp goes through the rest of its chunks
-    // without touching TMEM or global memory, for the others' barriers.
+    // After a wait that gave up the warp touches neither TMEM nor global memory, and at the next
+    // chunk's vote all eight leave together, so that none waits for another at a barrier.
     bool ok = true;
     auto look_ahead = [&](int i) {
       if (i >= n) return;
@@ -722,12 +722,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       t0 *= c2;
       t1 *= c2;
       // the reference maximum moves only on rises above kLazy, in any head or half
-      if (bar_or(1, 32 * kSoftmaxWarps, fresh || t0 > m0 + kLazy || t1 > m1 + kLazy)) {
+      if (bar_or(1, 32 * kSoftmaxWarps, !ok || fresh || t0 > m0 + kLazy || t1 > m1 + kLazy)) {
         if ((lane & 3) == 0) {
           sm->top[half][h0] = t0;
           sm->top[half][h1] = t1;
         }
-        bar_or(1, 32 * kSoftmaxWarps, 0u);
+        if (bar_or(1, 32 * kSoftmaxWarps, !ok)) break;
         t0 = fmaxf(t0, sm->top[half ^ 1][h0]);
         t1 = fmaxf(t1, sm->top[half ^ 1][h1]);
         const float n0 = t0 <= m0 + kLazy ? m0 : fmaxf(t0, m0), n1 = t1 <= m1 + kLazy ? m1 : fmaxf(t1, m1);
