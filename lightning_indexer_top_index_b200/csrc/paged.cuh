@@ -73,13 +73,10 @@ __device__ __forceinline__ void e2m1x8_to_bf16x2(uint32_t w, uint32_t (&o)[4]) {
 // half of them on the multiply pipe (the lookup above all runs on the integer
 // pipe, which bounds the attention's loader).
 struct E2m1Scale {
-  uint32_t s1, s2;
+  uint32_t c, s1;
   bool two;  // the same in all lanes of a converged warp
-  __device__ __forceinline__ explicit E2m1Scale(uint32_t c) {
-    s1 = c == 0xFFu ? 0x7FC0u : (min(c, 128u) + 126u) << 7;
-    s2 = c > 128u ? (c - 1u) << 7 : 0x3F80u;
-    s1 |= s1 << 16;
-    s2 |= s2 << 16;
+  __device__ __forceinline__ explicit E2m1Scale(uint32_t code) : c(code) {
+    s1 = (min(c, 128u) + 126u) * 0x00800080u;
     two = __any_sync(0xFFFFFFFFu, c > 128u);
   }
   __device__ __forceinline__ void expand(uint32_t w, uint32_t (&o)[4]) const {
@@ -91,6 +88,7 @@ struct E2m1Scale {
       o[i] = mul_bf16x2((y * 0x1040u) & 0x81C081C0u, s1);
     }
     if (two) {
+      const uint32_t s2 = (c == 0xFFu ? 0x7FC0u : c > 128u ? (c - 1u) << 7 : 0x3F80u) * 0x00010001u;
 #pragma unroll
       for (int i = 0; i < 4; i++) o[i] = mul_bf16x2(o[i], s2);
     }

@@ -166,22 +166,20 @@ __device__ __forceinline__ bool elect() {  // true in one lane of a converged wa
   return r != 0u;
 }
 
-// tc::mbar_wait with its loop kept rolled.
-__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile uint32_t *abort) {
+// tc::mbar_wait for a whole warp: the same answer in all lanes.  Its loop is
+// kept rolled, and the vote is in it, so that the warp stays together: with lane
+// 0 waiting and a shuffle of its answer, each hand-over between the roles was a
+// few hundred cycles longer (100 against 87 us for 256 queries of 1024 rows), with the lanes
+// looping apart and a vote at the end 88.5.  Polling without the hardware's
+// suspension (test_wait) takes issue slots from the others: 91.5.
+__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, volatile uint32_t *abort) {
 #pragma unroll 1
   for (uint32_t i = 0; i < tc::kWaitLimit; i++) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
+    if (__all_sync(0xFFFFFFFFu, tc::mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xFFFFFFFFu, *abort)) return false;
   }
   *abort = 1u;
   return false;
-}
-
-// A whole warp waits: the same answer in all lanes.  (With lane 0 waiting and a
-// shuffle of its answer, each hand-over between the roles was 100 cycles longer:
-// 100 against 90 us for 256 queries of 1024 rows.)
-__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, volatile uint32_t *abort) {
-  return __all_sync(0xFFFFFFFFu, wait_for(bar, parity, abort));
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {  // 2 ulp; 2^-inf = 0
@@ -586,10 +584,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok) {  // a wait gave up: the copies and products in flight end before the CTA does
       volatile uint32_t unused = 0;
-      if (!q_there) wait_for(&sm->q_full, (begun - 1) & 1, &unused);
+      if (!q_there) wait_all(&sm->q_full, (begun - 1) & 1, &unused);
       if (elect()) tc::mma_commit(&sm->drained[0]);
       __syncwarp();
-      wait_for(&sm->drained[0], 0, &unused);
+      wait_all(&sm->drained[0], 0, &unused);
     }
   } else if (warp == kIssueO) {
     // ------------------------------------------------- O^T += X^T . P^T, by a warp of its own: neither product waits for the other's turn
@@ -633,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       volatile uint32_t unused = 0;
       if (elect()) tc::mma_commit(&sm->drained[1]);
       __syncwarp();
-      wait_for(&sm->drained[1], 0, &unused);
+      wait_all(&sm->drained[1], 0, &unused);
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -975,9 +973,10 @@ __global__ void __launch_bounds__(kMergeThreads, 2) paged_attn_merge_kernel(cons
       L[k] = e[k] * l[k];
       R[k] = e[k] * r[k];
 #pragma unroll
-      for (int o = 1; o < kFew; o <<= 1) {
-        L[k] += __shfl_xor_sync(0xFFFFFFFFu, L[k], o);
-        R[k] += __shfl_xor_sync(0xFFFFFFFFu, R[k], o);
+      for (int o = 1; o < kFew; o <<= 1) R[k] += __shfl_xor_sync(0xFFFFFFFFu, R[k], o);
+      if (d0 == 0) {  // lse is written with the first dims
+#pragma unroll
+        for (int o = 1; o < kFew; o <<= 1) L[k] += __shfl_xor_sync(0xFFFFFFFFu, L[k], o);
       }
     }
 #pragma unroll 2
