@@ -262,15 +262,21 @@ struct Fmt {
   static constexpr int kRowsPerIter = 32 / kPieces;
 };
 
+// Eight E4M3 codes times their block's scale (both halves of s) as bf16.
+__device__ __forceinline__ uint4 expand_e4m3(uint32_t x, uint32_t y, uint32_t s) {
+  return make_uint4(mul_bf16x2(e4m3x2_to_bf16x2(x), s), mul_bf16x2(e4m3x2_to_bf16x2(x >> 16), s),
+                    mul_bf16x2(e4m3x2_to_bf16x2(y), s), mul_bf16x2(e4m3x2_to_bf16x2(y >> 16), s));
+}
+
 // Piece p of row r expanded to bf16 into the quarter's panels at x.  Lanes of
 // the second panel take their 16-byte chunks in another order, so that the
 // eight lanes that store together hit all banks.
 template <int kFmt>
-__device__ __forceinline__ void store_piece(uint8_t *x, int r, int p, const uint4 &v, uint32_t scale, bool on) {
+__device__ __forceinline__ void store_piece(uint8_t *x, int r, int p, const uint4 &v, uint32_t scale) {
   uint8_t *row = x + r * 128 + (p / (Fmt<kFmt>::kPieces / 2)) * kPanel;
   const int swz = r & 7;
   if constexpr (kFmt == LIDX_BF16) {
-    if (on) *reinterpret_cast<uint4 *>(row + (((p & 7) ^ swz) << 4)) = v;
+    *reinterpret_cast<uint4 *>(row + (((p & 7) ^ swz) << 4)) = v;
   } else if constexpr (kFmt == LIDX_E2M1) {
     const int turn = p & 2;
     const uint32_t w[4] = {turn ? v.z : v.x, turn ? v.w : v.y, turn ? v.x : v.z, turn ? v.y : v.w};
@@ -279,19 +285,33 @@ __device__ __forceinline__ void store_piece(uint8_t *x, int r, int p, const uint
     for (int i = 0; i < 4; i++) {
       uint32_t o[4];
       s.expand(w[i], o);
-      if (on) *reinterpret_cast<uint4 *>(row + (((4 * (p & 1) + (i ^ turn)) ^ swz) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4 *>(row + (((4 * (p & 1) + (i ^ turn)) ^ swz) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   } else {
     const int turn = (p >> 2) & 1;
     const uint32_t w[4] = {turn ? v.z : v.x, turn ? v.w : v.y, turn ? v.x : v.z, turn ? v.y : v.w};
     const uint32_t s = e8m0_to_bf16x2(scale);
 #pragma unroll
+    for (int i = 0; i < 2; i++)
+      *reinterpret_cast<uint4 *>(row + (((2 * (p & 3) + (i ^ turn)) ^ swz) << 4)) = expand_e4m3(w[2 * i], w[2 * i + 1], s);
+  }
+}
+
+// The same of a quarter with one panel of codes, in pieces of half the size.
+template <int kFmt>
+__device__ __forceinline__ void store_half_piece(uint8_t *x, int r, int p, const uint4 &v, uint32_t scale) {
+  uint8_t *row = x + r * 128;
+  const int swz = r & 7;
+  if constexpr (kFmt == LIDX_E2M1) {
+    const E2m1Scale s(scale);
+#pragma unroll
     for (int i = 0; i < 2; i++) {
-      const uint4 o = make_uint4(mul_bf16x2(e4m3x2_to_bf16x2(w[2 * i]), s), mul_bf16x2(e4m3x2_to_bf16x2(w[2 * i] >> 16), s),
-                                 mul_bf16x2(e4m3x2_to_bf16x2(w[2 * i + 1]), s),
-                                 mul_bf16x2(e4m3x2_to_bf16x2(w[2 * i + 1] >> 16), s));
-      if (on) *reinterpret_cast<uint4 *>(row + (((2 * (p & 3) + (i ^ turn)) ^ swz) << 4)) = o;
+      uint32_t o[4];
+      s.expand(i ? v.y : v.x, o);
+      *reinterpret_cast<uint4 *>(row + (((2 * p + i) ^ swz) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
     }
+  } else {
+    *reinterpret_cast<uint4 *>(row + ((p ^ swz) << 4)) = expand_e4m3(v.x, v.y, e8m0_to_bf16x2(scale));
   }
 }
 
@@ -469,7 +489,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t pitch = kFmt == LIDX_BF16 ? 2 * kv.ld : kv.ld;
     const uint8_t *scales = kv.scale + (kFmt == LIDX_E2M1 ? piece : piece / 4);
     const uint8_t *rope = static_cast<const uint8_t *>(kv.rope) + (lane % 8) * 16;
-    const bool in_last = !kQuant || piece < F::kPieces / 2;  // the last quarter has codes for its first panel only
+    // the last quarter has codes for its first panel only: the lanes take half as many of it
+    const uint8_t *last_data = data + 3 * (F::kPieces * 16) - piece * 8;
+    const uint8_t *last_scales = kv.scale + (kFmt == LIDX_E2M1 ? 12 + piece / 2 : 6);
     uint4 v[4][F::kIters], rv[2];
     uint32_t sc[4][F::kIters];
 #pragma unroll 1
@@ -495,12 +517,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           uint8_t *x = sX + stage * kXBytes + 2 * q * kPanel;
 #pragma unroll
-          for (int it = 0; it < F::kIters; it++)
-            store_piece<kFmt>(x, from + it * F::kRowsPerIter + lane / F::kPieces, piece, v[q][it], sc[q][it], q < 3 || in_last);
+          for (int it = 0; it < F::kIters; it++) {
+            const int r = from + it * F::kRowsPerIter + lane / F::kPieces;
+            if (kQuant && q == 3) store_half_piece<kFmt>(x, r, piece, v[q][it], sc[q][it]);
+            else store_piece<kFmt>(x, r, piece, v[q][it], sc[q][it]);
+          }
           if (kQuant && q == 3) {
 #pragma unroll
             for (int it = 0; it < 2; it++)
-              store_piece<LIDX_BF16>(x + kPanel, from + it * 4 + lane / 8, lane % 8, rv[it], 0u, true);
+              store_piece<LIDX_BF16>(x + kPanel, from + it * 4 + lane / 8, lane % 8, rv[it], 0u);
           }
           if (q & 1) {
             tc::fence_proxy_async_smem();
@@ -513,7 +538,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int it = 0; it < F::kIters; it++) {
             v[q][it] = make_uint4(0, 0, 0, 0);
             sc[q][it] = 127u;
-            if (row[it] >= 0 && (q < 3 || in_last)) {
+            if (row[it] >= 0 && kQuant && q == 3) {
+              const uint2 h = fetch(reinterpret_cast<const uint2 *>(last_data + row[it] * pitch));
+              v[q][it].x = h.x;
+              v[q][it].y = h.y;
+              sc[q][it] = fetch(last_scales + row[it] * kv.ld_scale);
+            } else if (row[it] >= 0) {
               v[q][it] = fetch(reinterpret_cast<const uint4 *>(data + row[it] * pitch + q * (F::kPieces * 16)));
               if (kQuant) sc[q][it] = fetch(scales + row[it] * kv.ld_scale + q * (kFmt == LIDX_E2M1 ? 4 : 2));
             }
