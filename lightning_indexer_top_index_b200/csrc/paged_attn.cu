@@ -22,11 +22,10 @@
 //   * one warp issues S[head][row] = Q . X^T (M = 64, N = 64, K = 512) and
 //     another, when the chunk's probabilities are there, O^T[d][head] +=
 //     X^T . P^T (M = 128 four times, N = 64, K = 64), both on tcgen05 with fp32
-//     accumulators in TMEM, two of S and one of O.  (One warp that polled for
-//     whichever was ready cost 300 to 700 cycles a product: 123 against 102 us
-//     for 256 queries of 1024 rows.  S in two or four accumulators, whose
-//     products need not wait for one another, cost the softmax warps as much as
-//     it gained: 104 us.);
+//     accumulators in TMEM, two of S and one of O.  (Before the waits were as
+//     cheap as below, one warp that polled for whichever was ready took 123 us
+//     instead of 102 for 256 queries of 1024 rows, and S in two or four
+//     accumulators, whose products need not wait for one another, 104.);
 //   * eight softmax warps, one per 16 heads and half of the chunk's rows, read
 //     S in the 16x256b shape, in which the 32 lanes of a warp share the 16 heads
 //     of its TMEM quarter (8 head pairs x 4 column groups), so row maxima take
@@ -41,6 +40,14 @@
 //   one and a row that has nearly all of it comes out exactly (by the unrounded
 //   sum the error over peaked rows was 1.6 times that of an exact P); lse takes
 //   the unrounded sum.
+//
+// What bounds it.  For 256 queries of 1024 rows in E2M1 (85 us, 20 at the bf16
+// rate of the matrix products) a CTA takes a chunk every 3700 cycles.  Its
+// products (32 of 32 cycles, 16 of 48, both bound by their operands in shared
+// memory) take 1800 of them; a loader warp, always busy, takes all of them for
+// its 550 instructions, with half of all issue slots used, 9000 instructions a
+// chunk, a quarter of them in the expansion.  Sixteen loader warps of half as
+// much each leave the others fewer slots and registers: 94 us.
 //
 // The loops are kept small (one place each for a product, a load, a store):
 // unrolled over their chunks they outgrew the instruction cache, and the
