@@ -9,6 +9,10 @@
 // four steps).  The dots are whole numbers below 2^21.  Each lane folds its 8
 // heads' ReLU'd dots with 64-bit weights and the 8 lanes of a block add up.  A
 // dot becomes a double by its bits (2^52 + n, minus 2^52), which costs an add.
+// A step is bound by the latency of its chain, so the four tiles' products are
+// issued in turn, and the weights are read from shared memory, so that
+// the products and the next step's codes have registers (32 rows of 128 blocks
+// a CTA: 8.5 -> 8.0 us; with the codes of two steps ahead it gained nothing).
 //
 // Selection.  Scores become order-preserving 64-bit keys in shared memory
 // (0: not eligible, all ones: always taken).  Few keys are ranked directly, a
@@ -39,8 +43,10 @@ constexpr int kMaxCluster = 8;
 constexpr int kMaxSlice = 16384;  // keys a CTA holds
 constexpr int kMaxK = 256;
 constexpr int kDigit = 11, kBins = 1 << kDigit;
+constexpr int kLinear = 512;      // bins of the scores' range (2048: 18.1 us for 512 rows of 256 blocks instead of 17.6)
 constexpr int kCand = 256;        // keys of a bin ranked directly
-constexpr int kDirect = 128;      // keys of a row ranked directly without binning
+constexpr int kDirect = 128;      // keys of a row ranked directly without binning (with 64: 8.0 -> 8.5 us for 128
+                                  // a CTA; with 256: 10.3 -> 12.4 us for 244)
 constexpr int kPitch = 144;       // bytes between a head's codes: 16-byte reads of 8 heads x 4 lanes hit all banks
 constexpr uint64_t kForced = ~0ull;
 
@@ -128,17 +134,19 @@ __device__ __forceinline__ float value_of(uint64_t key) {  // monotone in the ke
 
 // The bin that holds the want-th largest of sm.hist's `bins` counted keys,
 // from above: sm.bin, sm.above (keys in the bins above it), sm.bin_count.
+template <int kN>
 __device__ __forceinline__ void find_bin(Smem &sm, uint32_t want) {
-  const int tid = threadIdx.x, per = kBins / kThreads;  // thread t sums bins from the top on
+  constexpr int per = kN / kThreads;
+  const int tid = threadIdx.x;  // thread t sums bins from the top on
   uint32_t mine = 0;
 #pragma unroll
-  for (int i = 0; i < per; i++) mine += sm.hist[kBins - 1 - (tid * per + i)];
+  for (int i = 0; i < per; i++) mine += sm.hist[kN - 1 - (tid * per + i)];
   uint32_t before, zero, total, zero2;
   scan2(sm, mine, 0u, before, zero, total, zero2);
   if (before < want && want <= before + mine) {
     uint32_t at = before;
     for (int i = 0; i < per; i++) {
-      const int bin = kBins - 1 - (tid * per + i);
+      const int bin = kN - 1 - (tid * per + i);
       const uint32_t h = sm.hist[bin];
       if (want <= at + h) {
         sm.bin = bin;
@@ -214,7 +222,7 @@ __device__ __noinline__ void kth_by_radix(Smem &sm, const uint64_t *keys, int n,
         atomicAdd(&sm.hist[static_cast<uint32_t>(x >> shift) & (bins - 1)], 1u);
     }
     __syncthreads();
-    find_bin(sm, want);
+    find_bin<kBins>(sm, want);
     prefix = (top == 64 ? 0ull : prefix << (top - shift)) | sm.bin;
     want -= sm.above;
     count = sm.bin_count;
@@ -244,18 +252,18 @@ __device__ __forceinline__ void kth_largest(Smem &sm, const uint64_t *keys, int 
                                             float hi) {
   const int tid = threadIdx.x;
   // infinities, NaN ranges and equal scores: everything in bin 0
-  float per_bin = (kBins - 1) / (hi - lo);
+  float per_bin = (kLinear - 1) / (hi - lo);
   if (!(per_bin < 3e38f) || !(hi - lo < 3e38f)) per_bin = 0.f;
   auto bin_of = [&](uint64_t key) {
-    return min(max(static_cast<int>((value_of(key) - lo) * per_bin), 0), kBins - 1);
+    return min(max(static_cast<int>((value_of(key) - lo) * per_bin), 0), kLinear - 1);
   };
-  for (int i = tid; i < kBins; i += kThreads) sm.hist[i] = 0u;
+  for (int i = tid; i < kLinear; i += kThreads) sm.hist[i] = 0u;
   if (tid == 0) sm.n_cand = 0u;
   __syncthreads();
   for (int i = tid; i < n; i += kThreads)
     if (ranked(keys[i])) atomicAdd(&sm.hist[bin_of(keys[i])], 1u);
   __syncthreads();
-  find_bin(sm, k);
+  find_bin<kLinear>(sm, k);
   if (sm.bin_count > kCand) {
     kth_by_radix(sm, keys, n, count, k);
     return;
@@ -443,7 +451,6 @@ __global__ void __launch_bounds__(kThreads, 2) block_select_kernel(const lidx_bl
   }
   __syncthreads();
   uint32_t A[4][4][4];  // [tile][step][register]
-  double weight[8];
 #pragma unroll
   for (int m = 0; m < 4; m++) {
 #pragma unroll
@@ -455,12 +462,12 @@ __global__ void __launch_bounds__(kThreads, 2) block_select_kernel(const lidx_bl
       A[m][1][half] = x.z; A[m][1][2 + half] = x.w;
       A[m][2][half] = y.x; A[m][2][2 + half] = y.y;
       A[m][3][half] = y.z; A[m][3][2 + half] = y.w;
-      weight[2 * m + half] = sm.weight[h];
     }
   }
 
   // ---- scores
   const int heads_tiles = (a.H + 15) / 16;
+  const volatile double *weight = sm.weight + g;
   float lo = INFINITY, hi = -INFINITY;
   uint32_t some = 0, must = 0;
 #pragma unroll 1
@@ -471,20 +478,38 @@ __global__ void __launch_bounds__(kThreads, 2) block_select_kernel(const lidx_bl
     const uint4 x = k.x, y = k.y;
     // lane (g, c) ends with heads g, g + 8 of each tile for blocks j + 2c, j + 2c + 1
     double s0 = 0., s1 = 0.;
+    int d[4][4] = {};
+    // the tiles' products in turn, as each step of a tile waits for the one before
+    if (heads_tiles > 2) {
+#pragma unroll
+      for (int m = 0; m < 4; m++) mma_s8(d[m], A[m][0], x.x, x.y);
+#pragma unroll
+      for (int m = 0; m < 4; m++) mma_s8(d[m], A[m][1], x.z, x.w);
+#pragma unroll
+      for (int m = 0; m < 4; m++) mma_s8(d[m], A[m][2], y.x, y.y);
+#pragma unroll
+      for (int m = 0; m < 4; m++) mma_s8(d[m], A[m][3], y.z, y.w);
+    } else {
+#pragma unroll
+      for (int m = 0; m < 2; m++) mma_s8(d[m], A[m][0], x.x, x.y);
+#pragma unroll
+      for (int m = 0; m < 2; m++) mma_s8(d[m], A[m][1], x.z, x.w);
+#pragma unroll
+      for (int m = 0; m < 2; m++) mma_s8(d[m], A[m][2], y.x, y.y);
+#pragma unroll
+      for (int m = 0; m < 2; m++) mma_s8(d[m], A[m][3], y.z, y.w);
+    }
+    double r0 = 0., r1 = 0.;
 #pragma unroll
     for (int m = 0; m < 4; m++) {
-      if (m < heads_tiles) {
-        int d[4] = {0, 0, 0, 0};
-        mma_s8(d, A[m][0], x.x, x.y);
-        mma_s8(d, A[m][1], x.z, x.w);
-        mma_s8(d, A[m][2], y.x, y.y);
-        mma_s8(d, A[m][3], y.z, y.w);
-        s0 = fma(whole(max(d[0], 0)), weight[2 * m], s0);
-        s1 = fma(whole(max(d[1], 0)), weight[2 * m], s1);
-        s0 = fma(whole(max(d[2], 0)), weight[2 * m + 1], s0);
-        s1 = fma(whole(max(d[3], 0)), weight[2 * m + 1], s1);
-      }
+      const double wa = weight[16 * m], wb = weight[16 * m + 8];
+      s0 = fma(whole(max(d[m][0], 0)), wa, s0);
+      s1 = fma(whole(max(d[m][1], 0)), wa, s1);
+      r0 = fma(whole(max(d[m][2], 0)), wb, r0);
+      r1 = fma(whole(max(d[m][3], 0)), wb, r1);
     }
+    s0 += r0;
+    s1 += r1;
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, o);
