@@ -24,7 +24,7 @@
 // come out ascending by a prefix sum; equal keys are taken from the lowest
 // index on.
 //
-// A row's blocks are split over a cluster of up to 8 CTAs when there are few
+// A row's blocks are split over a cluster of up to 16 CTAs when there are few
 // rows; every CTA selects its k best, pushes them into the first CTA's shared
 // memory, and that one selects among them in the same way (the slices are
 // contiguous, so the lists stay in index order).
@@ -39,11 +39,13 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
+constexpr int kMaxBlocks = 8 * 16384;  // of a sequence: what 8 CTAs hold, where the device has no clusters of 16
 constexpr int kMaxSlice = 16384;  // keys a CTA holds
 constexpr int kMaxK = 256;
 constexpr int kDigit = 11, kBins = 1 << kDigit;
 constexpr int kLinear = 512;      // bins of the scores' range (2048: 18.1 us for 512 rows of 256 blocks instead of 17.6)
+constexpr int kLong = 8192;       // blocks of a row from which on more than four rows take clusters of 16
 constexpr int kCand = 256;        // keys of a bin ranked directly
 constexpr int kDirect = 128;      // keys of a row ranked directly without binning (with 64: 8.0 -> 8.5 us for 128
                                   // a CTA; with 256: 10.3 -> 12.4 us for 244)
@@ -636,13 +638,50 @@ __global__ void __launch_bounds__(kThreads, 2) block_select_kernel(const lidx_bl
   if (tid == 0 && a.n_sel) a.n_sel[bt] = n_sel;
 }
 
+size_t smem_of(int g, int slice, int k) {
+  return sizeof(Smem) + static_cast<size_t>(slice) * 8 + (g > 1 ? static_cast<size_t>(g) * k * 12 : 0);
+}
+
+// Does the current device run clusters of 16 CTAs, as large as they get here?
+bool cluster16_ok() {
+  static int cache[64] = {};  // by device: 0 not asked yet, 1 yes, 2 no
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return false;
+  }
+  if (!cache[dev]) {
+    const size_t smem = smem_of(16, kMaxBlocks / 16, kMaxK);
+    cudaFuncSetAttribute(block_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaFuncSetAttribute(block_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 16;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, block_select_kernel, &cfg);
+    cudaGetLastError();
+    cache[dev] = e == cudaSuccess && n >= 1 ? 1 : 2;
+  }
+  return cache[dev] == 1;
+}
+
 // CTAs a row is split over: so that a slice fits, and, while the rows leave
-// SMs idle, down to 128 blocks a CTA.
+// SMs idle, down to 128 blocks a CTA.  Sixteen for one to four rows (1954
+// blocks: 10.5 -> 9.9 us, 62500: 87 -> 53), and for up to nine long ones (9 x
+// 14000: 26.2 -> 23.6; 9 x 2000 would go from 10.7 to 11.9).
 int cluster_for(const lidx_block_select_args &a) {
+  const int64_t rows = static_cast<int64_t>(a.B) * a.T;
   int g = 1;
-  while (g < kMaxCluster && (a.max_pages > g * kMaxSlice ||
-                             (a.max_pages > g * 128 && static_cast<int64_t>(a.B) * a.T * g * 2 <= 148)))
-    g *= 2;
+  while (g < 8 && (a.max_pages > g * kMaxSlice || (a.max_pages > g * 128 && rows * g * 2 <= 148))) g *= 2;
+  if (g == 8 && a.max_pages > 8 * 128 && rows * 16 <= 148 && (rows <= 4 || a.max_pages > kLong) && cluster16_ok()) g = 16;
   return g;
 }
 
@@ -651,14 +690,16 @@ int slice_of(const lidx_block_select_args &a, int g) { return ((a.max_pages + g 
 }  // namespace
 
 bool block_select_supported(const lidx_block_select_args &a) {
-  return a.k <= kMaxK && a.H <= 64 && slice_of(a, cluster_for(a)) <= kMaxSlice;
+  return a.k <= kMaxK && a.H <= 64 && a.max_pages <= kMaxBlocks;
 }
 
 cudaError_t launch_block_select(const lidx_block_select_args &a, void *ws, cudaStream_t st) {
   const int g = cluster_for(a), slice = slice_of(a, g);
-  const size_t smem = sizeof(Smem) + static_cast<size_t>(slice) * 8 + (g > 1 ? static_cast<size_t>(g) * a.k * 12 : 0);
+  const size_t smem = smem_of(g, slice, a.k);
   cudaError_t e = cudaFuncSetAttribute(block_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
+  if (e == cudaSuccess && g > 8)
+    e = cudaFuncSetAttribute(block_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(g * a.B * a.T));

@@ -343,6 +343,25 @@ def test_select(cuda_device, H, T, B, P, rows, k):
     assert np.array_equal(ids, want)
 
 
+@pytest.mark.parametrize("B,n_blocks,k", [(1, 1025, 16), (4, 1100, 100), (7, 8300, 30), (10, 8300, 30), (2, 131072, 256),
+                                          (40, 16390, 5)])
+def test_select_long_rows(cuda_device, B, n_blocks, k):
+    """Rows that clusters of every size share, up to the longest; pages shared by the sequences."""
+    g = np.random.default_rng(B + n_blocks)
+    P = 16
+    n_pages = 5000
+    table = g.integers(0, n_pages, (B, n_blocks)).astype(np.int32)
+    codes, scale = _summaries(g, n_pages)
+    q = g.standard_normal((B, 1, 3, 128)).astype(np.float32)
+    w = (g.random((B, 1, 3)) - 0.3).astype(np.float32)
+    lens = [n_blocks * P] + [int(n_blocks * P * g.random()) for _ in range(B - 1)]
+    ids, n_sel, status, qb = _select(q, w, codes, scale, table, P, lens, k)
+    assert status == 0
+    want, wn = ref.select(qb, w, codes, scale, table, P, n_pages, lens, k, 1, 2)
+    assert np.array_equal(n_sel, wn)
+    assert np.array_equal(ids, want)
+
+
 @pytest.mark.parametrize("n_blocks", [700, 5000])
 @pytest.mark.parametrize("n_first,n_last,k", [(0, 0, 7), (1, 2, 3), (0, 9, 20), (4, 0, 256)])
 def test_select_ties(cuda_device, n_blocks, n_first, n_last, k):
