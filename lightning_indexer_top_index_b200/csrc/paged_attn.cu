@@ -434,19 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       job = sm->job;
       c = sm->chunk;
     }
-    if (lane == 0) {  // does a job that began in the CTA before continue here, and is this its second CTA?
-      Split sp;
-      sp.job = -1;
-      sp.start = my0 - c;
-      sp.end = 0;
-      sp.total = total;
-      const Deal deal(total, jobs.G);
-      if (c > 0 && deal.start(static_cast<int32_t>(blockIdx.x) - 1) <= sp.start) {
-        sp.job = job;
-        sp.end = sp.start + (job_rows(a, job, gs, shift) + kRows - 1) / kRows;
-      }
-      ws.split[blockIdx.x] = sp;
-    }
+    const int32_t first_job = job, first_c = c;
     for (int i = 0; i < n; i++) {
       uint32_t flags = 0u;
       if (left == 0) {  // a job begins: the CTA's first, or the next one with rows
@@ -483,6 +471,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) tc::mbar_arrive(&sm->ring_full[slot]);
       c++;
       left--;
+    }
+    if (lane == 0) {  // does a job that began in the CTA before continue here, and is this its second CTA?
+      Split sp;
+      sp.job = -1;
+      sp.start = my0 - first_c;
+      sp.end = 0;
+      sp.total = total;
+      const Deal deal(total, jobs.G);
+      if (first_c > 0 && deal.start(static_cast<int32_t>(blockIdx.x) - 1) <= sp.start) {
+        sp.job = first_job;
+        sp.end = sp.start + (job_rows(a, first_job, gs, shift) + kRows - 1) / kRows;
+      }
+      ws.split[blockIdx.x] = sp;
     }
     if (bounds) raise_status(ws.status, LIDX_DEV_BOUNDS);
   } else if (warp >= kSoftmaxWarps && warp < kIssueS) {
@@ -869,36 +870,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 16; k++) v[k] = __uint_as_float(next[k]);
             if (q + 2 < 16) tmem_ld16_issue(tmem + quarter + kOCol + 16 * (q + 2), next);
             if (out_now) {
-              // an 8 x 8 exchange among eight lanes: lane = dim, registers = heads, to a lane with eight dims of a head
-              uint32_t w1[8], w2[8], w3[8];
+              // Lane = dim, registers = heads.  Two lanes swap halves, the even one's for the odd heads, so
+              // that each has two dims of every other head: a store writes 64 bytes of two heads.
               const uint32_t pick = (lane & 1) ? 0x3276u : 0x5410u;  // odd: other's high, own high half; even: own low, other's low
+              uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + (out_row + hb + (lane & 1)) * kD + (d & ~1));
 #pragma unroll
               for (int k = 0; k < 8; k++) {
-                const __nv_bfloat162 two =
-                    __floats2bfloat162_rn(v[2 * k] * sm->l[hb + 2 * k], v[2 * k + 1] * sm->l[hb + 2 * k + 1]);
+                const float2 l2 = *reinterpret_cast<const float2 *>(&sm->l[hb + 2 * k]);
+                const __nv_bfloat162 two = __floats2bfloat162_rn(v[2 * k] * l2.x, v[2 * k + 1] * l2.y);
                 const uint32_t own = *reinterpret_cast<const uint32_t *>(&two);
-                w1[k] = __byte_perm(own, __shfl_xor_sync(0xFFFFFFFFu, own, 1), pick);  // head 2k + lane % 2
-              }
-#pragma unroll
-              for (int k = 0; k < 4; k++) {  // head 4k + lane % 4: words 2k, 2k + 1
-                const bool odd = lane & 2;
-                const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? w1[2 * k] : w1[2 * k + 1], 2);
-                w2[2 * k] = odd ? other : w1[2 * k];
-                w2[2 * k + 1] = odd ? w1[2 * k + 1] : other;
-              }
-              uint16_t *o = static_cast<uint16_t *>(a.out) + (out_row + hb + (lane & 7)) * kD + (d & ~7);
-#pragma unroll
-              for (int k = 0; k < 2; k++) {  // head 8k + lane % 8: words 4k .. 4k + 3
-                const bool odd = lane & 4;
-#pragma unroll
-                for (int j = 0; j < 2; j++) {
-                  const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? w2[4 * k + j] : w2[4 * k + 2 + j], 4);
-                  w3[4 * k + j] = odd ? other : w2[4 * k + j];
-                  w3[4 * k + 2 + j] = odd ? w2[4 * k + 2 + j] : other;
-                }
-                if (hb + 8 * k + (lane & 7) < heads)
-                  *reinterpret_cast<uint4 *>(o + 8 * k * kD) =
-                      make_uint4(w3[4 * k], w3[4 * k + 1], w3[4 * k + 2], w3[4 * k + 3]);
+                const uint32_t w = __byte_perm(own, __shfl_xor_sync(0xFFFFFFFFu, own, 1), pick);
+                if (hb + 2 * k + (lane & 1) < heads) o[k * kD] = w;
               }
             } else {
               float4 *o = ws.o + (slot_o * (kH / 4) + hb / 4) * kD + d;
