@@ -74,10 +74,14 @@ __device__ __forceinline__ void e2m1x8_to_bf16x2(uint32_t w, uint32_t (&o)[4]) {
 // pipe, which bounds the attention's loader).
 struct E2m1Scale {
   uint32_t c, s1;
-  bool two;  // the same in all lanes of a converged warp
-  __device__ __forceinline__ explicit E2m1Scale(uint32_t code) : c(code) {
-    s1 = (min(c, 128u) + 126u) * 0x00800080u;
-    two = __any_sync(0xFFFFFFFFu, c > 128u);
+  bool two;  // with kWarp (a converged warp) the same in all lanes
+  template <bool kWarp = true>
+  __device__ __forceinline__ static E2m1Scale of(uint32_t code) {
+    E2m1Scale s;
+    s.c = code;
+    s.s1 = (min(code, 128u) + 126u) * 0x00800080u;
+    s.two = kWarp ? __any_sync(0xFFFFFFFFu, code > 128u) != 0 : code > 128u;
+    return s;
   }
   __device__ __forceinline__ void expand(uint32_t w, uint32_t (&o)[4]) const {
     const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
@@ -128,6 +132,21 @@ struct Dims8 {
       }
       scale = fetch(kv.scale + p * kv.ld_scale + d0 / (kFmt == LIDX_E4M3 ? 64 : 32));
     }
+  }
+
+  // as bf16, where the cache is not fp32: the exact products, rounded where the scale takes them out of its range
+  __device__ __forceinline__ uint4 bf16() const {
+    if (kFmt == LIDX_E4M3 && codes) {
+      const uint32_t s = e8m0_to_bf16x2(scale);
+      return make_uint4(mul_bf16x2(e4m3x2_to_bf16x2(w[0].x), s), mul_bf16x2(e4m3x2_to_bf16x2(w[0].x >> 16), s),
+                        mul_bf16x2(e4m3x2_to_bf16x2(w[0].y), s), mul_bf16x2(e4m3x2_to_bf16x2(w[0].y >> 16), s));
+    }
+    if (kFmt == LIDX_E2M1 && codes) {
+      uint32_t o[4];
+      E2m1Scale::of<false>(scale).expand(w[0].x, o);
+      return make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    return w[0];
   }
 
   __device__ __forceinline__ void values(float (&v)[8]) const {

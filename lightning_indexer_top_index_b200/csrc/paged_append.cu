@@ -229,7 +229,9 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const lidx_paged
 }
 
 // Rows as values: dim/8 threads a row, thread t dims [8t, 8t + 8), kPer rows of
-// it in flight together.
+// it in flight together.  The instructions bound it: as bf16 the values come
+// from bf16 products of code and scale (through fp32, and rounded with a look
+// for NaNs, the 20011 rows took 3 us more).
 template <int kFmt, int kPer>
 __global__ void __launch_bounds__(kThreads) paged_read_kernel(const lidx_paged_read_args a, int shift,
                                                                uint32_t *status) {
@@ -256,6 +258,11 @@ __global__ void __launch_bounds__(kThreads) paged_read_kernel(const lidx_paged_r
 #pragma unroll
   for (int r = 0; r < kPer; r++) {
     if (seq[r] < 0) continue;
+    if (kFmt != LIDX_F32 && a.out_dtype == LIDX_BF16) {
+      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + (i0 + r) * a.ld_out + 8 * t) =
+          p[r] >= 0 ? raw[r].bf16() : make_uint4(0, 0, 0, 0);
+      continue;
+    }
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (p[r] >= 0) raw[r].values(v);
     if (a.out_dtype == LIDX_F32) {
@@ -285,8 +292,8 @@ cudaError_t launch_paged_append(const lidx_paged_append_args &a, void *ws, cudaS
 }
 
 // Few rows are read one a thread; from about a machine full of threads on,
-// four (20011 rows of 512 in 4 bits: 13.1 us against 17.0 with one; 64 rows
-// 4.0 us with one).
+// four (20011 rows of 512 in 4 bits, with their append: 22.5 us against 26.7
+// with one; 64 rows 4.6 us with one and 5.3 with four).
 constexpr int64_t kManyThreads = 148 * 2048;
 
 cudaError_t launch_paged_read(const lidx_paged_read_args &a, void *ws, cudaStream_t st) {

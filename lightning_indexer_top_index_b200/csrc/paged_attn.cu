@@ -287,7 +287,7 @@ __device__ __forceinline__ void store_piece(uint8_t *x, int r, int p, const uint
   } else if constexpr (kFmt == LIDX_E2M1) {
     const int turn = p & 2;
     const uint32_t w[4] = {turn ? v.z : v.x, turn ? v.w : v.y, turn ? v.x : v.z, turn ? v.y : v.w};
-    const E2m1Scale s(scale);
+    const E2m1Scale s = E2m1Scale::of(scale);
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       uint32_t o[4];
@@ -310,7 +310,7 @@ __device__ __forceinline__ void store_half_piece(uint8_t *x, int r, int p, const
   uint8_t *row = x + r * 128;
   const int swz = r & 7;
   if constexpr (kFmt == LIDX_E2M1) {
-    const E2m1Scale s(scale);
+    const E2m1Scale s = E2m1Scale::of(scale);
 #pragma unroll
     for (int i = 0; i < 2; i++) {
       uint32_t o[4];

@@ -203,6 +203,36 @@ def test_append_nonfinite(cuda_device):
     assert ref.bf16_value(p[2][3])[52] == np.inf
 
 
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3", "bf16"])
+@pytest.mark.parametrize("dim", [512, 128])
+@pytest.mark.parametrize("n", [7, 9000])
+def test_read_bf16_every_scale(cuda_device, fmt, dim, n):
+    """Rows read as bf16 under every scale byte: the exact products, rounded once; few rows and many, some of
+    them padding or not there."""
+    g = np.random.default_rng(dim + n)
+    P = 16
+    table = g.permutation(40).astype(np.int32).reshape(2, 20)
+    table[1, 19] = -1
+    c = _cache(g, fmt, dim, 40, P, table, pad=1)
+    if fmt != "bf16":
+        c.rows.scale.copy_(torch.from_numpy(g.permutation(c.rows.scale.numel()).astype(np.uint8).reshape(c.rows.scale.shape)))
+    seq, row = g.integers(0, 2, n).astype(np.int32), g.integers(0, 20 * P, n).astype(np.int32)
+    seq[3] = -1
+    seq[5], row[5] = 1, 19 * P + 2
+    out = torch.full((n, dim + 8), 7.0, dtype=torch.bfloat16, device=DEV)
+    call = L.paged_read_call(c, _i32(seq), _i32(row), out=out[:, :dim])
+    call()
+    assert call.status() == L.DEV_BOUNDS
+    page = table[np.maximum(seq, 0), row // P]
+    with np.errstate(all="ignore"):
+        want = torch.from_numpy(_values(c, fmt)[np.maximum(page, 0) * P + row % P].astype(np.float64)).to(torch.bfloat16).float().numpy()
+    want[(page < 0) & (seq >= 0)] = 0.0
+    want[seq < 0] = 7.0
+    got = out.float().cpu().numpy()
+    assert np.array_equal(got[:, :dim], want, equal_nan=True)
+    assert (got[:, dim:] == 7.0).all()
+
+
 # -------------------------------------------------------------------- pool
 @pytest.mark.parametrize("fmt", ["e4m3", "e2m1", "bf16", "f32"])
 @pytest.mark.parametrize("P", [16, 64, 256])
