@@ -53,6 +53,7 @@
 // unrolled over their chunks they outgrew the instruction cache, and the
 // kernel spent half its time fetching code (a chunk took 8000 cycles).
 #include <algorithm>
+#include <type_traits>
 
 #include "paged.cuh"
 #include "quant.cuh"
@@ -79,7 +80,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 32.f;            // base-2 headroom of the reference maximum
 constexpr int kMergeThreads = 256;
-constexpr int kFew = 8;                  // partials that one warp joins
+constexpr int kFew = 8, kSome = 32;      // partials that one warp joins, for 128 dims and for 32
 constexpr int kBatch = 10;               // partials that a warp of the merge has in flight: two batches of 148 / 8
 constexpr int kMergeCtas = 4;            // of the merge, for an SM
 constexpr int kMaxCtas = 256;            // one CTA per SM
@@ -914,17 +915,18 @@ __device__ __forceinline__ float weight_of(float m, float M) { return m == M ? 1
 // Joins the partial results of jobs that span CTAs.  An item is such a job,
 // four of its heads and 32 or 128 of its dims (lane = dim).  First the partials'
 // weights are found, a lane or a thread for each partial, then the weighted sum
-// runs over the partials, in their order.  Where a job has few of them, as with
-// many short jobs, a warp joins an item by itself; where it has many, the eight
-// warps of the CTA take every eighth partial each and their sums meet in shared
-// memory.  It is bound by the latency of a few dependent reads of L2, so what
+// runs over the partials, in their order.  Where a job has up to 32 of them, as
+// with many short jobs, a warp joins an item by itself; where it has more, the
+// eight warps of the CTA take every eighth partial each and their sums meet in
+// shared memory (8 sequences of 15000 rows, 19 partials a job: 61 us so, 48 by a
+// warp).  It is bound by the latency of a few dependent reads of L2, so what
 // helps is many of them in flight (112 registers): held to 80 registers for a third CTA on the
 // SM it took 1 to 2 us more.
 __global__ void __launch_bounds__(kMergeThreads, 2) paged_attn_merge_kernel(const lidx_paged_attn_args a, const Jobs jobs,
                                                                          const Scratch ws) {
   constexpr int kWarps = kMergeThreads / 32, kItems = (kH / 4) * (kD / 32);
-  __shared__ Split list[kMaxCtas];  // jobs with few partials from the front, with many from the back
-  __shared__ int32_t count[2][kWarps];
+  __shared__ Split list[3][kMaxCtas];  // jobs with few, some and many partials
+  __shared__ int32_t count[3][kWarps];
   __shared__ float4 weight_s[kMaxCtas], acc_s[kWarps][32], red_s[3][kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
@@ -933,25 +935,30 @@ __global__ void __launch_bounds__(kMergeThreads, 2) paged_attn_merge_kernel(cons
   Split sp;
   sp.job = -1;
   if (tid < jobs.G) sp = ws.split[tid];
-  bool many = false;
+  int kind = -1;
   if (sp.job >= 0) {
     const Deal deal(sp.total, jobs.G);
-    many = deal.owner(sp.end - 1) - deal.owner(sp.start) >= kFew;
+    const int n = deal.owner(sp.end - 1) - deal.owner(sp.start) + 1;
+    kind = n <= kFew ? 0 : n <= kSome ? 1 : 2;
   }
-  const uint32_t few_mask = __ballot_sync(0xFFFFFFFFu, sp.job >= 0 && !many), many_mask = __ballot_sync(0xFFFFFFFFu, many);
-  if (lane == 0) {
-    count[0][warp] = __popc(few_mask);
-    count[1][warp] = __popc(many_mask);
+  int n_of[3], at = 0;
+#pragma unroll
+  for (int c = 0; c < 3; c++) {
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, kind == c);
+    if (lane == 0) count[c][warp] = __popc(mask);
+    if (kind == c) at = __popc(mask & ((1u << lane) - 1u));
   }
   __syncthreads();
-  int n_few = 0, n_many = 0, at = __popc((many ? many_mask : few_mask) & ((1u << lane) - 1u));
 #pragma unroll
-  for (int w = 0; w < kWarps; w++) {
-    if (w < warp) at += count[many][w];
-    n_few += count[0][w];
-    n_many += count[1][w];
+  for (int c = 0; c < 3; c++) {
+    n_of[c] = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+      if (w < warp && kind == c) at += count[c][w];
+      n_of[c] += count[c][w];
+    }
   }
-  if (sp.job >= 0) list[many ? kMaxCtas - 1 - at : at] = sp;
+  if (kind >= 0) list[kind][at] = sp;
   __syncthreads();
 
   float m[4], l[4], r[4], e[4];  // of four heads of the partial that the thread looks after
@@ -974,52 +981,59 @@ __global__ void __launch_bounds__(kMergeThreads, 2) paged_attn_merge_kernel(cons
     if (a.lse && d0 == 0 && lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
   };
 
+  // by a warp: kLanes >= the partials, kJ * 32 dims
+  auto join = [&](const Split *jobs_of, int n_jobs, auto lanes_c, auto j_c) {
+    constexpr int kLanes = decltype(lanes_c)::value, kJ = decltype(j_c)::value, kPer = kItems / kJ;
 #pragma unroll 1
-  for (int item = blockIdx.x * kWarps + warp; item < n_few * kItems / 4; item += gridDim.x * kWarps) {  // 128 dims each
-    const Split sj = list[item / (kItems / 4)];
-    const int h4 = (item % (kItems / 4)) / 4, d0 = 128 * (item % 4);
-    const Deal deal(sj.total, jobs.G);
-    const int32_t from = deal.owner(sj.start), n = deal.owner(sj.end - 1) - from + 1;  // <= kFew
-    const int part = lane % kFew;  // the lane's partial
-    look(part < n ? ws.ml + slot_of(deal, from + part, sj.start) * kH + 4 * h4 : nullptr);
-    float M[4], L[4], R[4], A[4][4] = {};
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-      M[k] = m[k];
-#pragma unroll
-      for (int o = 1; o < kFew; o <<= 1) M[k] = fmaxf(M[k], __shfl_xor_sync(0xFFFFFFFFu, M[k], o));
-      e[k] = part < n ? weight_of(m[k], M[k]) : 0.f;
-      L[k] = e[k] * l[k];
-      R[k] = e[k] * r[k];
-#pragma unroll
-      for (int o = 1; o < kFew; o <<= 1) R[k] += __shfl_xor_sync(0xFFFFFFFFu, R[k], o);
-      if (d0 == 0) {  // lse is written with the first dims
-#pragma unroll
-        for (int o = 1; o < kFew; o <<= 1) L[k] += __shfl_xor_sync(0xFFFFFFFFu, L[k], o);
-      }
-    }
-#pragma unroll 2
-    for (int c = 0; c < n; c++) {
-      const float4 *o = ws.o + static_cast<size_t>(slot_of(deal, from + c, sj.start) * (kH / 4) + h4) * kD + d0 + lane;
-      float4 v[4];
-#pragma unroll
-      for (int j = 0; j < 4; j++) v[j] = o[32 * j];
+    for (int item = blockIdx.x * kWarps + warp; item < n_jobs * kPer; item += gridDim.x * kWarps) {
+      const Split sj = jobs_of[item / kPer];
+      constexpr int kSlices = kD / (32 * kJ);
+      const int h4 = (item % kPer) / kSlices, d0 = 32 * kJ * (item % kSlices);
+      const Deal deal(sj.total, jobs.G);
+      const int32_t from = deal.owner(sj.start), n = deal.owner(sj.end - 1) - from + 1;
+      const int part = lane % kLanes;  // the lane's partial
+      look(part < n ? ws.ml + slot_of(deal, from + part, sj.start) * kH + 4 * h4 : nullptr);
+      float M[4], L[4], R[4], A[4][kJ] = {};
 #pragma unroll
       for (int k = 0; k < 4; k++) {
-        const float w = __shfl_sync(0xFFFFFFFFu, e[k], c);
+        M[k] = m[k];
 #pragma unroll
-        for (int j = 0; j < 4; j++) A[k][j] = fmaf(w, reinterpret_cast<const float *>(&v[j])[k], A[k][j]);
+        for (int o = 1; o < kLanes; o <<= 1) M[k] = fmaxf(M[k], __shfl_xor_sync(0xFFFFFFFFu, M[k], o));
+        e[k] = part < n ? weight_of(m[k], M[k]) : 0.f;
+        L[k] = e[k] * l[k];
+        R[k] = e[k] * r[k];
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) R[k] += __shfl_xor_sync(0xFFFFFFFFu, R[k], o);
+        if (d0 == 0) {  // lse is written with the first dims
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) L[k] += __shfl_xor_sync(0xFFFFFFFFu, L[k], o);
+        }
       }
+#pragma unroll (8 / kJ)
+      for (int c = 0; c < n; c++) {
+        const float4 *o = ws.o + static_cast<size_t>(slot_of(deal, from + c, sj.start) * (kH / 4) + h4) * kD + d0 + lane;
+        float4 v[kJ];
+#pragma unroll
+        for (int j = 0; j < kJ; j++) v[j] = o[32 * j];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          const float w = __shfl_sync(0xFFFFFFFFu, e[k], c);
+#pragma unroll
+          for (int j = 0; j < kJ; j++) A[k][j] = fmaf(w, reinterpret_cast<const float *>(&v[j])[k], A[k][j]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+#pragma unroll
+        for (int j = 0; j < kJ; j++) write(sj, 4 * h4 + k, d0 + 32 * j, M[k], L[k], R[k], A[k][j]);
     }
-#pragma unroll
-    for (int k = 0; k < 4; k++)
-#pragma unroll
-      for (int j = 0; j < 4; j++) write(sj, 4 * h4 + k, d0 + 32 * j, M[k], L[k], R[k], A[k][j]);
-  }
+  };
+  join(list[0], n_of[0], std::integral_constant<int, kFew>(), std::integral_constant<int, 4>());
+  join(list[1], n_of[1], std::integral_constant<int, kSome>(), std::integral_constant<int, 1>());
 
 #pragma unroll 1
-  for (int item = blockIdx.x; item < n_many * kItems; item += gridDim.x) {
-    const Split sj = list[kMaxCtas - 1 - item / kItems];
+  for (int item = blockIdx.x; item < n_of[2] * kItems; item += gridDim.x) {
+    const Split sj = list[2][item / kItems];
     const int h4 = (item % kItems) / (kD / 32), d0 = 32 * (item % (kD / 32));
     const Deal deal(sj.total, jobs.G);
     const int32_t from = deal.owner(sj.start), n = deal.owner(sj.end - 1) - from + 1;  // <= kMaxCtas
