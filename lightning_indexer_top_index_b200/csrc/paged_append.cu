@@ -9,10 +9,10 @@
 // rotated ones, the pairs whose angles it evaluates (one, or four), so that no
 // value or angle is handed from lane to lane: with the rotated dims held 16 a
 // lane by four lanes and their angles fetched by shuffles, 20011 rows of 512,
-// appended and read back, took 28.4 us instead of 25.6.  An angle is formed as pos * inv_freq / 2 pi
-// turns in 64 bits and its whole turns dropped before it is rounded to fp32
-// (error below 2^-25 turns at any position), since in fp32 the product alone
-// would be off by up to pos * 2^-24 radians.
+// appended and read back, took 28.4 us instead of 25.6.  An angle is formed as
+// pos * inv_freq / 2 pi turns in 64 bits and its whole turns dropped before it
+// is rounded to fp32 (error below 2^-25 turns at any position), since in fp32
+// the product alone would be off by up to pos * 2^-24 radians.
 #include "paged.cuh"
 #include "quant.cuh"
 

@@ -920,8 +920,8 @@ __device__ __forceinline__ float weight_of(float m, float M) { return m == M ? 1
 // eight warps of the CTA take every eighth partial each and their sums meet in
 // shared memory (8 sequences of 15000 rows, 19 partials a job: 61 us so, 48 by a
 // warp).  It is bound by the latency of a few dependent reads of L2, so what
-// helps is many of them in flight (112 registers): held to 80 registers for a third CTA on the
-// SM it took 1 to 2 us more.
+// helps is many of them in flight (112 registers): held to 80 registers for a
+// third CTA on the SM it took 1 to 2 us more.
 __global__ void __launch_bounds__(kMergeThreads, 2) paged_attn_merge_kernel(const lidx_paged_attn_args a, const Jobs jobs,
                                                                          const Scratch ws) {
   constexpr int kWarps = kMergeThreads / 32, kItems = (kH / 4) * (kD / 32);
