@@ -35,16 +35,14 @@
 //     TMEM: at 8 one of the 64 heads made most chunks pay for it.  Sums are of
 //     the fp32 probabilities; floating point loses nothing by a common factor
 //     up to 2^32.
-//   P is rounded to bf16 for the second product, at most 2^-8 of each probability.  O
-//   is divided by the sum of the rounded ones, so that its weights add up to
-//   one and a row that has nearly all of it comes out exactly (by the unrounded
-//   sum the error over peaked rows was 1.6 times that of an exact P); lse takes
-//   the unrounded sum.
+//   P enters the second product as its bf16 value and the bf16 value of what
+//   that rounding left, so it keeps 16 bits (2^-16 of each probability), as in
+//   the attention over linear caches; both are products of the same rows.
 //
-// What bounds it.  For 256 queries of 1024 rows in E2M1 (85 us, 20 at the bf16
+// What bounds it.  For 256 queries of 1024 rows in E2M1 (86 us, 20 at the bf16
 // rate of the matrix products) a CTA takes a chunk every 3700 cycles.  Its
-// products (32 of 32 cycles, 16 of 48, both bound by their operands in shared
-// memory) take 1800 of them; a loader warp, always busy, takes all of them for
+// products (32 of 32 cycles, 32 of 48, both bound by their operands in shared
+// memory) take 2560 of them; a loader warp, always busy, takes all of them for
 // its 550 instructions, with half of all issue slots used, 9000 instructions a
 // chunk, a quarter of them in the expansion.  Sixteen loader warps of half as
 // much each leave the others fewer slots and registers: 94 us.
@@ -74,7 +72,8 @@ constexpr int kRing = 4;                 // chunks the scout may be ahead
 constexpr int kPanel = 64 * 128;         // one 64-line panel of X or Q: 64 dims
 constexpr int kXBytes = 8 * kPanel;
 constexpr int kQBytes = 8 * kPanel;
-constexpr int kPBytes = kH * kRows * 2;
+constexpr int kPHalf = kH * kRows * 2;   // P as bf16, then what its rounding left
+constexpr int kPBytes = 2 * kPHalf;
 constexpr uint32_t kOCol = 128;          // S of stage i at columns 64 i, O^T tile t at columns kOCol + 64 t
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -110,14 +109,15 @@ struct __align__(16) Smem {
   uint32_t abort;
   float alpha[kH];                // rescale factors of a chunk
   float top[2][kH];               // a chunk's maxima, by half of its rows
-  float sums[2][kH][2];           // a job's sums, by half of the rows
-  float l[kH];                    // 1 / sum of the rounded probabilities
+  float sums[2][kH];              // a job's sums, by half of the rows
+  float l[kH];                    // 1 / sum
   // the CTA's first chunk
   int32_t job, chunk;
   int32_t scan[kThreads / 32];
 };
 
-constexpr size_t smem_bytes() { return 1024 + kQBytes + 2 * kXBytes + 2 * kPBytes + sizeof(Smem); }
+constexpr size_t smem_bytes() { return kQBytes + 2 * kXBytes + 2 * kPBytes + sizeof(Smem); }
+static_assert(smem_bytes() <= 227 * 1024, "a CTA's shared memory");
 
 // A job that spans CTAs, written by the second of them: its chunks are
 // [start, end) of all chunks (job -1: the CTA is no job's second one).
@@ -129,7 +129,7 @@ struct __align__(16) Split {
 struct Scratch {
   uint32_t *status;
   Split *split;  // [G]
-  float4 *ml;    // [2 * G][kH]: maximum, sum, sum of the rounded probabilities
+  float2 *ml;    // [2 * G][kH]: maximum, sum
   float4 *o;     // [2 * G][kH / 4][kD], four heads together: as TMEM holds them
 };
 
@@ -346,8 +346,7 @@ template <int kFmt>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ lidx_paged_attn_args a,
                       const Jobs jobs, const int shift, const Scratch ws) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle wants panels at multiples of 1024
   uint8_t *sQ = smem;
   uint8_t *sX = sQ + kQBytes;      // stage i at sX + i * kXBytes
   uint8_t *sP = sX + 2 * kXBytes;  // stage i at sP + i * kPBytes
@@ -658,8 +657,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < kRows / 16; kk++) {
 #pragma unroll
-            for (int k = dt; k < dt + 2; k++)
-              tc::mma_bf16(tmem + kOCol + 64 * k, xd + ((2 * k * kPanel + kk * 2048) >> 4), pd + kk * 2, idesc, !first || kk > 0);
+            for (int k = dt; k < dt + 2; k++) {
+              const uint64_t x = xd + ((2 * k * kPanel + kk * 2048) >> 4);
+              tc::mma_bf16(tmem + kOCol + 64 * k, x, pd + kk * 2, idesc, !first || kk > 0);
+              tc::mma_bf16(tmem + kOCol + 64 * k, x, pd + kk * 2 + (kPHalf >> 4), idesc, true);
+            }
           }
           tc::mma_commit(&sm->x_free[i & 1][dt / 2]);
         }
@@ -694,9 +696,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool negative = a.scale < 0.f;
     const float c2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
     const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    // the reference maximum is the same in both halves; the sums are of this half's rows (r: of the
-    // rounded probabilities)
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, r0 = 0.f, r1 = 0.f;
+    // the reference maximum is the same in both halves; the sums are of this half's rows
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     bool first_segment = true;  // the CTA's first job
     bool fresh = true;          // nothing of the job is in O yet
     uint32_t next_valid = 0u, next_flags = 0u;  // what the scout says about the next chunk
@@ -775,8 +776,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         m1 = n1;
         l0 *= a0;
         l1 *= a1;
-        r0 *= a0;
-        r1 *= a1;
         if (!fresh) {  // rescale O^T (lane = dim, columns = heads), when the last second product is done
           if (half == 0 && (lane & 3) == 0) {
             sm->alpha[h0] = a0;
@@ -812,11 +811,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         l1 += y0 + y1;
         const __nv_bfloat162 px = __floats2bfloat162_rn(x0, x1), py = __floats2bfloat162_rn(y0, y1);
         const uint32_t wx = *reinterpret_cast<const uint32_t *>(&px), wy = *reinterpret_cast<const uint32_t *>(&py);
-        r0 += bf16x2_lo(wx) + bf16x2_hi(wx);
-        r1 += bf16x2_lo(wy) + bf16x2_hi(wy);
+        const __nv_bfloat162 qx = __floats2bfloat162_rn(x0 - bf16x2_lo(wx), x1 - bf16x2_hi(wx));
+        const __nv_bfloat162 qy = __floats2bfloat162_rn(y0 - bf16x2_lo(wy), y1 - bf16x2_hi(wy));
         const int at = ((4 * half + u) ^ (h0 & 7)) << 4;
         *reinterpret_cast<uint32_t *>(p0 + at) = wx;
         *reinterpret_cast<uint32_t *>(p1 + at) = wy;
+        *reinterpret_cast<uint32_t *>(p0 + kPHalf + at) = *reinterpret_cast<const uint32_t *>(&qx);
+        *reinterpret_cast<uint32_t *>(p1 + kPHalf + at) = *reinterpret_cast<const uint32_t *>(&qy);
       }
       tc::fence_proxy_async_smem();
       tc::tc_fence_before();
@@ -831,28 +832,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int o = 1; o < 4; o <<= 1) {
           l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, o);
           l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, o);
-          r0 += __shfl_xor_sync(0xFFFFFFFFu, r0, o);
-          r1 += __shfl_xor_sync(0xFFFFFFFFu, r1, o);
         }
         const int h = (lane & 1) ? h1 : h0;  // lanes with lane % 4 < 2 look after a head each
-        float l = (lane & 1) ? l1 : l0, rounded = (lane & 1) ? r1 : r0;
+        float l = (lane & 1) ? l1 : l0;
         const float m = (lane & 1) ? m1 : m0;
-        if ((lane & 3) < 2) {
-          sm->sums[half][h][0] = l;
-          sm->sums[half][h][1] = rounded;
-        }
+        if ((lane & 3) < 2) sm->sums[half][h] = l;
         bar_or(1, 32 * kSoftmaxWarps, 0u);
         const int heads = min(kH, a.H - g * kH);
         const int64_t out_row = static_cast<int64_t>(bt) * a.H + g * kH;
         const int64_t slot_o = 2 * static_cast<int64_t>(blockIdx.x) + (first_segment ? 0 : 1);
         if ((lane & 3) < 2 && half == 0 && ok) {
-          l += sm->sums[1][h][0];
-          rounded += sm->sums[1][h][1];
+          l += sm->sums[1][h];
           if (out_now) {
-            sm->l[h] = rounded == 0.f ? 0.f : 1.f / rounded;
+            sm->l[h] = l == 0.f ? 0.f : 1.f / l;
             if (a.lse && h < heads) a.lse[out_row + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
           } else {
-            ws.ml[slot_o * kH + h] = make_float4(m, l, rounded, 0.f);
+            ws.ml[slot_o * kH + h] = make_float2(m, l);
           }
         }
         bar_or(1, 32 * kSoftmaxWarps, 0u);  // sm->l is in
@@ -894,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm->o_free);
         m0 = m1 = -INFINITY;
-        l0 = l1 = r0 = r1 = 0.f;
+        l0 = l1 = 0.f;
         first_segment = false;
         fresh = true;
       }
@@ -927,7 +922,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) paged_attn_merge_kernel(cons
   constexpr int kWarps = kMergeThreads / 32, kItems = (kH / 4) * (kD / 32);
   __shared__ Split list[3][kMaxCtas];  // jobs with few, some and many partials
   __shared__ int32_t count[3][kWarps];
-  __shared__ float4 weight_s[kMaxCtas], acc_s[kWarps][32], red_s[3][kWarps];
+  __shared__ float4 weight_s[kMaxCtas], acc_s[kWarps][32], red_s[2][kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   pdl_wait();  // the partial results come from the previous kernel
@@ -961,23 +956,22 @@ __global__ void __launch_bounds__(kMergeThreads, 2) paged_attn_merge_kernel(cons
   if (kind >= 0) list[kind][at] = sp;
   __syncthreads();
 
-  float m[4], l[4], r[4], e[4];  // of four heads of the partial that the thread looks after
-  auto look = [&](const float4 *ml) {
+  float m[4], l[4], e[4];  // of four heads of the partial that the thread looks after
+  auto look = [&](const float2 *ml) {
 #pragma unroll
     for (int k = 0; k < 4; k++) {
-      const float4 x = ml ? ml[k] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      const float2 x = ml ? ml[k] : make_float2(-INFINITY, 0.f);
       m[k] = x.x;
       l[k] = x.y;
-      r[k] = x.z;
     }
   };
   // the job is the CTA's first one unless the CTA began with an earlier job
   auto slot_of = [&](const Deal &deal, int32_t c, int32_t start) { return 2 * c + (deal.start(c) < start ? 1 : 0); };
-  auto write = [&](const Split &sj, int h, int d0, float M, float L, float R, float A) {  // head h of the job's group
+  auto write = [&](const Split &sj, int h, int d0, float M, float L, float A) {  // head h of the job's group
     const int32_t bt = sj.job >> jobs.group_shift, group = sj.job & ((1 << jobs.group_shift) - 1);
     if (group * kH + h >= a.H) return;
     const int64_t row = static_cast<int64_t>(bt) * a.H + group * kH + h;
-    static_cast<__nv_bfloat16 *>(a.out)[row * kD + d0 + lane] = __float2bfloat16_rn(A * (R == 0.f ? 0.f : 1.f / R));
+    static_cast<__nv_bfloat16 *>(a.out)[row * kD + d0 + lane] = __float2bfloat16_rn(A * (L == 0.f ? 0.f : 1.f / L));
     if (a.lse && d0 == 0 && lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
   };
 
@@ -993,7 +987,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) paged_attn_merge_kernel(cons
       const int32_t from = deal.owner(sj.start), n = deal.owner(sj.end - 1) - from + 1;
       const int part = lane % kLanes;  // the lane's partial
       look(part < n ? ws.ml + slot_of(deal, from + part, sj.start) * kH + 4 * h4 : nullptr);
-      float M[4], L[4], R[4], A[4][kJ] = {};
+      float M[4], L[4], A[4][kJ] = {};
 #pragma unroll
       for (int k = 0; k < 4; k++) {
         M[k] = m[k];
@@ -1001,13 +995,8 @@ __global__ void __launch_bounds__(kMergeThreads, 2) paged_attn_merge_kernel(cons
         for (int o = 1; o < kLanes; o <<= 1) M[k] = fmaxf(M[k], __shfl_xor_sync(0xFFFFFFFFu, M[k], o));
         e[k] = part < n ? weight_of(m[k], M[k]) : 0.f;
         L[k] = e[k] * l[k];
-        R[k] = e[k] * r[k];
 #pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) R[k] += __shfl_xor_sync(0xFFFFFFFFu, R[k], o);
-        if (d0 == 0) {  // lse is written with the first dims
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) L[k] += __shfl_xor_sync(0xFFFFFFFFu, L[k], o);
-        }
+        for (int o = 1; o < kLanes; o <<= 1) L[k] += __shfl_xor_sync(0xFFFFFFFFu, L[k], o);
       }
 #pragma unroll (8 / kJ)
       for (int c = 0; c < n; c++) {
@@ -1025,7 +1014,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) paged_attn_merge_kernel(cons
 #pragma unroll
       for (int k = 0; k < 4; k++)
 #pragma unroll
-        for (int j = 0; j < kJ; j++) write(sj, 4 * h4 + k, d0 + 32 * j, M[k], L[k], R[k], A[k][j]);
+        for (int j = 0; j < kJ; j++) write(sj, 4 * h4 + k, d0 + 32 * j, M[k], L[k], A[k][j]);
     }
   };
   join(list[0], n_of[0], std::integral_constant<int, kFew>(), std::integral_constant<int, 4>());
@@ -1038,7 +1027,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) paged_attn_merge_kernel(cons
     const Deal deal(sj.total, jobs.G);
     const int32_t from = deal.owner(sj.start), n = deal.owner(sj.end - 1) - from + 1;  // <= kMaxCtas
     look(tid < n ? ws.ml + slot_of(deal, from + tid, sj.start) * kH + 4 * h4 : nullptr);
-    float M[4], L[4], R[4];
+    float M[4], L[4];
 #pragma unroll
     for (int k = 0; k < 4; k++) M[k] = warp_max(m[k]);
     if (lane == 0) red_s[0][warp] = make_float4(M[0], M[1], M[2], M[3]);
@@ -1051,13 +1040,9 @@ __global__ void __launch_bounds__(kMergeThreads, 2) paged_attn_merge_kernel(cons
     for (int k = 0; k < 4; k++) {
       e[k] = tid < n ? weight_of(m[k], M[k]) : 0.f;
       L[k] = warp_sum(tid < n ? e[k] * l[k] : 0.f);
-      R[k] = warp_sum(tid < n ? e[k] * r[k] : 0.f);
     }
     if (tid < n) weight_s[tid] = make_float4(e[0], e[1], e[2], e[3]);
-    if (lane == 0) {
-      red_s[1][warp] = make_float4(L[0], L[1], L[2], L[3]);
-      red_s[2][warp] = make_float4(R[0], R[1], R[2], R[3]);
-    }
+    if (lane == 0) red_s[1][warp] = make_float4(L[0], L[1], L[2], L[3]);
     __syncthreads();
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
@@ -1082,14 +1067,13 @@ __global__ void __launch_bounds__(kMergeThreads, 2) paged_attn_merge_kernel(cons
     acc_s[warp][lane] = acc;
     __syncthreads();
     if (warp < 4) {  // warp k finishes head k
-      float A = 0.f, Ls = 0.f, Rs = 0.f;
+      float A = 0.f, Ls = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; w++) {
         A += reinterpret_cast<const float *>(&acc_s[w][lane])[warp];
         Ls += reinterpret_cast<const float *>(&red_s[1][w])[warp];
-        Rs += reinterpret_cast<const float *>(&red_s[2][w])[warp];
       }
-      write(sj, 4 * h4 + warp, d0, warp == 0 ? M[0] : warp == 1 ? M[1] : warp == 2 ? M[2] : M[3], Ls, Rs, A);
+      write(sj, 4 * h4 + warp, d0, warp == 0 ? M[0] : warp == 1 ? M[1] : warp == 2 ? M[2] : M[3], Ls, A);
     }
     __syncthreads();
   }
@@ -1141,7 +1125,7 @@ bool paged_attn_supported(const lidx_paged_attn_args &a) {
 
 size_t paged_attn_workspace(const lidx_paged_attn_args &a) {
   const Jobs j = plan(a);
-  return LIDX_WS_HEADER + align256(j.G * sizeof(Split)) + static_cast<size_t>(j.G) * 2 * kH * (sizeof(float4) + kD * 4);
+  return LIDX_WS_HEADER + align256(j.G * sizeof(Split)) + static_cast<size_t>(j.G) * 2 * kH * (sizeof(float2) + kD * 4);
 }
 
 int paged_attn_launches(const lidx_paged_attn_args &) { return 2; }  // the attention and the merge
@@ -1154,8 +1138,8 @@ cudaError_t launch_paged_attn(const lidx_paged_attn_args &a, void *ws, cudaStrea
   p += LIDX_WS_HEADER;
   s.split = reinterpret_cast<Split *>(p);
   p += align256(j.G * sizeof(Split));
-  s.ml = reinterpret_cast<float4 *>(p);
-  p += static_cast<size_t>(j.G) * 2 * kH * sizeof(float4);
+  s.ml = reinterpret_cast<float2 *>(p);
+  p += static_cast<size_t>(j.G) * 2 * kH * sizeof(float2);
   s.o = reinterpret_cast<float4 *>(p);
   CUtensorMap tm;
   if (!make_tmap_3d(&tm, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kD, a.H, static_cast<uint64_t>(a.B) * a.T, 64, kH,

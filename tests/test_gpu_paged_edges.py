@@ -1,0 +1,53 @@
+"""Paged-cache calls where they can go wrong beside the ordinary cases: what
+the attention's probabilities keep, calls from several host threads and
+streams, selections among many near scores, values that are not numbers.
+
+Tolerances as derived in test_gpu_paged.py, but for the probabilities: they
+enter the second product as a bf16 value and the bf16 value of what its
+rounding left, together within 2^-16 of each."""
+import numpy as np
+import pytest
+import torch
+
+import _paged_ref as ref
+import lightning_indexer_top_index_b200 as L
+from test_gpu_paged import DEV, FMT, _i32, _table, _values
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ attend
+def cancelling_case(g, rows, heads):
+    """Rows in pairs (x, -x) in all but the first 16 dims, which alone meet the
+    queries: outputs nearly cancel, so that an error of a probability shows
+    beside the output's own rounding.  Values are exact in every format."""
+    x = g.choice(np.array([1.0, 2.0, 3.0, 4.0, 6.0]), (rows, 512)) * g.choice(np.array([-1.0, 1.0]), (rows, 512))
+    x[1::2, 16:] = -x[: rows - rows % 2: 2, 16:]
+    q = np.zeros((heads, 512))
+    q[:, :16] = g.standard_normal((heads, 16)) * 2.0 ** -8
+    return x, torch.from_numpy(q).bfloat16()
+
+
+def attn_bound(want, rows):
+    """Largest errors of out: its rounding, 2^-16 of each probability, what the
+    logits' error does to them, and two fp32 sums over the rows."""
+    wo, _, mag, big = want
+    d = 512 * 2.0 ** -24 * big[..., None]
+    return 2.0 ** -8 * np.abs(wo) + (2.0 ** -16 + np.expm1(2 * d) + 2 * rows * 2.0 ** -24) * 1.02 * mag + 1e-30
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3", "bf16"])
+@pytest.mark.parametrize("rows,heads", [(6, 64), (64, 70), (300, 16), (3000, 5)])
+def test_attn_probabilities_keep_16_bits(cuda_device, fmt, rows, heads):
+    g = np.random.default_rng(rows + heads)
+    P = 64
+    table, n_pages = _table(g, [rows], P)
+    c = L.PagedKV.empty(FMT[fmt], 512, n_pages, P, torch.from_numpy(table).to(DEV))
+    x, q = cancelling_case(g, rows, heads)
+    L.paged_append(torch.from_numpy(x.astype(np.float32)).to(DEV), c, _i32([0] * rows), _i32(range(rows)))
+    vals = _values(c, fmt)
+    assert np.array_equal(vals[[table[0, r // P] * P + r % P for r in range(rows)]], x)
+    want = ref.attend(q.double().numpy()[None, None], vals, table, P, n_pages, [rows], 1.0)
+    out, _ = L.paged_attn(q.to(DEV)[None, None], c, _i32([rows]), scale=1.0)
+    worst = (np.abs(out.cpu().double().numpy() - want[0]) / attn_bound(want, rows)).max()
+    assert worst <= 1.0, f"out off by {worst:.2f} of its bound"
