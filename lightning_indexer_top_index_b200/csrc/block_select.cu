@@ -29,6 +29,7 @@
 // memory, and that one selects among them in the same way (the slices are
 // contiguous, so the lists stay in index order).
 #include <algorithm>
+#include <atomic>
 
 #include "paged.cuh"
 #include "tc.cuh"
@@ -638,26 +639,33 @@ __global__ void __launch_bounds__(kThreads, 2) block_select_kernel(const lidx_bl
   if (tid == 0 && a.n_sel) a.n_sel[bt] = n_sel;
 }
 
-size_t smem_of(int g, int slice, int k) {
+constexpr size_t smem_of(int g, int slice, int k) {
   return sizeof(Smem) + static_cast<size_t>(slice) * 8 + (g > 1 ? static_cast<size_t>(g) * k * 12 : 0);
+}
+
+static_assert(smem_of(16, kMaxBlocks / 16, kMaxK) <= smem_of(8, kMaxSlice, kMaxK), "the largest is a cluster of 8's");
+
+// The same for every call of the process, so that calls from several threads agree.
+cudaError_t allow_largest() {
+  const cudaError_t e = allow_smem(block_select_kernel, smem_of(8, kMaxSlice, kMaxK));  // a cluster of 16 needs less
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(block_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
 // Does the current device run clusters of 16 CTAs, as large as they get here?
 bool cluster16_ok() {
-  static int cache[64] = {};  // by device: 0 not asked yet, 1 yes, 2 no
+  static std::atomic<int> cache[64];  // by device: 0 not asked yet, 1 yes, 2 no
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     cudaGetLastError();
     return false;
   }
-  if (!cache[dev]) {
-    const size_t smem = smem_of(16, kMaxBlocks / 16, kMaxK);
-    cudaFuncSetAttribute(block_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    cudaFuncSetAttribute(block_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  int known = cache[dev].load(std::memory_order_relaxed);
+  if (!known) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(16);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = smem_of(16, kMaxBlocks / 16, kMaxK);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 16;
@@ -666,11 +674,13 @@ bool cluster16_ok() {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, block_select_kernel, &cfg);
+    const bool ok = allow_largest() == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&n, block_select_kernel, &cfg) == cudaSuccess && n >= 1;
     cudaGetLastError();
-    cache[dev] = e == cudaSuccess && n >= 1 ? 1 : 2;
+    known = ok ? 1 : 2;
+    cache[dev].store(known, std::memory_order_relaxed);
   }
-  return cache[dev] == 1;
+  return known == 1;
 }
 
 // CTAs a row is split over: so that a slice fits, and, while the rows leave
@@ -696,10 +706,7 @@ bool block_select_supported(const lidx_block_select_args &a) {
 cudaError_t launch_block_select(const lidx_block_select_args &a, void *ws, cudaStream_t st) {
   const int g = cluster_for(a), slice = slice_of(a, g);
   const size_t smem = smem_of(g, slice, a.k);
-  cudaError_t e = cudaFuncSetAttribute(block_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e == cudaSuccess && g > 8)
-    e = cudaFuncSetAttribute(block_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  const cudaError_t e = allow_largest();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(g * a.B * a.T));

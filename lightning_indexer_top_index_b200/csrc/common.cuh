@@ -143,6 +143,16 @@ cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
+// Lets `kern` be launched with up to `most` bytes of dynamic shared memory.  The
+// limit belongs to the function on its device, not to the calling thread, so
+// `most` is what the largest call needs and the same in all of them: with each
+// call's own size, a thread with a smaller call lowers the limit between
+// another's setting it and its launch, which then fails.
+template <typename Kern>
+cudaError_t allow_smem(Kern kern, size_t most) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+}
+
 // Device status word at the start of a workspace.
 __device__ __forceinline__ void raise_status(uint32_t *status, uint32_t flag) {
   if (status) atomicOr(status, flag);

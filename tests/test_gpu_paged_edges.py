@@ -5,6 +5,8 @@ streams, selections among many near scores, values that are not numbers.
 Tolerances as derived in test_gpu_paged.py, but for the probabilities: they
 enter the second product as a bf16 value and the bf16 value of what its
 rounding left, together within 2^-16 of each."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -51,3 +53,48 @@ def test_attn_probabilities_keep_16_bits(cuda_device, fmt, rows, heads):
     out, _ = L.paged_attn(q.to(DEV)[None, None], c, _i32([rows]), scale=1.0)
     worst = (np.abs(out.cpu().double().numpy() - want[0]) / attn_bound(want, rows)).max()
     assert worst <= 1.0, f"out off by {worst:.2f} of its bound"
+
+
+# ------------------------------------------------- several threads and streams
+def _many_threads(calls, times):
+    """Every call `times` times, each from a thread and on a stream of its own; the errors."""
+    errors, start = [], threading.Barrier(len(calls))
+
+    def work(call):
+        stream = torch.cuda.Stream()
+        start.wait()
+        for _ in range(times):
+            try:
+                call(stream)
+            except Exception as e:
+                errors.append(str(e))
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    return errors
+
+
+def test_select_from_several_threads(cuda_device):
+    """Calls whose shared memory differs, from several host threads at once."""
+    g = np.random.default_rng(50)
+    P, n_pages = 16, 300
+    codes = torch.from_numpy(g.integers(-127, 128, (n_pages, 128), dtype=np.int8)).to(DEV)
+    scale = torch.rand(n_pages, device=DEV) + 0.5
+    calls, want = [], []
+    for width, k in ((131072, 256), (40, 4), (16000, 200), (300, 16)):
+        lens = _i32([min(width, 500) * P])
+        table = _i32(g.integers(0, n_pages, (1, width)))
+        q = torch.from_numpy(g.standard_normal((1, 1, 8, 128)).astype(np.float32)).to(DEV).bfloat16()
+        w = torch.rand(1, 1, 8, device=DEV)
+        call = L.block_select_call(q, w, codes, scale, table, P, lens, k)
+        want.append(call()[0].clone())
+        calls.append(call)
+    torch.cuda.synchronize()
+    errors = _many_threads(calls, 4000)
+    assert not errors, f"{len(errors)} calls failed: {errors[0]}"
+    for call, ids in zip(calls, want):
+        assert torch.equal(call.out[0], ids)
