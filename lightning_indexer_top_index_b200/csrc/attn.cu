@@ -19,6 +19,7 @@ namespace {
 constexpr int kD = 512;
 constexpr int kRC = 32;          // rows per CTA
 constexpr int kThreads = 256;
+constexpr int kMaxH = 64;
 constexpr int kXs = kD + 4;      // padded row stride (floats): conflict-free float4 row reads
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -225,6 +226,8 @@ __global__ void __launch_bounds__(128) attn_merge_kernel(lidx_attn_args a, const
     a.lse[static_cast<size_t>(b) * H + h] = L > 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
+constexpr size_t smem_of(int H) { return (static_cast<size_t>(H) * kD + kRC * kXs + H * kRC) * sizeof(float); }
+
 int n_splits(const lidx_attn_args &a) {
   const int rows = a.n_ids + a.swa_len;
   return rows > 0 ? (rows + kRC - 1) / kRC : 1;
@@ -266,24 +269,24 @@ cudaError_t launch_attn(const lidx_attn_args &a, void *ws, cudaStream_t st) {
   float *part_o = reinterpret_cast<float *>(static_cast<char *>(ws) + LIDX_WS_HEADER);
   float2 *part_ml = reinterpret_cast<float2 *>(static_cast<char *>(ws) + LIDX_WS_HEADER + part_o_bytes(a, ns));
   if (attn_tc_supported(a)) return launch_attn_tc(a, part_o, part_ml, ns, status, st);
-  const size_t smem = (static_cast<size_t>(a.H) * kD + kRC * kXs + a.H * kRC) * sizeof(float);
+  const size_t smem = smem_of(a.H);
+  cudaError_t e;
   dim3 grid(ns, a.B);
   switch (a.kv.dtype) {
     case LIDX_F32:
-      cudaFuncSetAttribute(attn_cc_kernel<LIDX_F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if ((e = allow_smem(attn_cc_kernel<LIDX_F32>, smem_of(kMaxH))) != cudaSuccess) return e;
       attn_cc_kernel<LIDX_F32><<<grid, kThreads, smem, st>>>(a, part_o, part_ml, ns, status);
       break;
     case LIDX_BF16:
-      cudaFuncSetAttribute(attn_cc_kernel<LIDX_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if ((e = allow_smem(attn_cc_kernel<LIDX_BF16>, smem_of(kMaxH))) != cudaSuccess) return e;
       attn_cc_kernel<LIDX_BF16><<<grid, kThreads, smem, st>>>(a, part_o, part_ml, ns, status);
       break;
     default:
-      cudaFuncSetAttribute(attn_cc_kernel<LIDX_E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if ((e = allow_smem(attn_cc_kernel<LIDX_E4M3>, smem_of(kMaxH))) != cudaSuccess) return e;
       attn_cc_kernel<LIDX_E4M3><<<grid, kThreads, smem, st>>>(a, part_o, part_ml, ns, status);
       break;
   }
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_attn_merge(a, part_o, part_ml, ns, st);
 }
 

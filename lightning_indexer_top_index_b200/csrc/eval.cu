@@ -16,6 +16,10 @@ namespace lidx {
 namespace {
 
 constexpr int kD = 512;
+constexpr int kMaxH = 64;
+constexpr size_t kMaxRowBytes = 200u * 1024u;  // of a row of probabilities in shared memory
+
+constexpr size_t prob_smem(int H) { return (static_cast<size_t>(H) * kD + H) * sizeof(float); }
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int KT>
@@ -453,22 +457,22 @@ cudaError_t launch_eval(const lidx_eval_args &a, void *ws, cudaStream_t st) {
   } else if (a.ops & LIDX_EVAL_GOLDEN) {
     float *lse2 = reinterpret_cast<float *>(cur);
     cur += lse_bytes(a);
-    const size_t smem = (static_cast<size_t>(a.H) * kD + a.H) * sizeof(float);
+    const size_t smem = prob_smem(a.H);
     dim3 g2((a.N + 127) / 128, a.L * a.T);
     switch (a.kv.dtype) {
       case LIDX_F32:
         golden_lse_kernel<LIDX_F32><<<a.L * a.T * a.H, 256, 0, st>>>(a, lse2);
-        cudaFuncSetAttribute(golden_prob_kernel<LIDX_F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if ((e = allow_smem(golden_prob_kernel<LIDX_F32>, prob_smem(kMaxH))) != cudaSuccess) return e;
         golden_prob_kernel<LIDX_F32><<<g2, 128, smem, st>>>(a, lse2);
         break;
       case LIDX_BF16:
         golden_lse_kernel<LIDX_BF16><<<a.L * a.T * a.H, 256, 0, st>>>(a, lse2);
-        cudaFuncSetAttribute(golden_prob_kernel<LIDX_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if ((e = allow_smem(golden_prob_kernel<LIDX_BF16>, prob_smem(kMaxH))) != cudaSuccess) return e;
         golden_prob_kernel<LIDX_BF16><<<g2, 128, smem, st>>>(a, lse2);
         break;
       default:
         golden_lse_kernel<LIDX_E4M3><<<a.L * a.T * a.H, 256, 0, st>>>(a, lse2);
-        cudaFuncSetAttribute(golden_prob_kernel<LIDX_E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if ((e = allow_smem(golden_prob_kernel<LIDX_E4M3>, prob_smem(kMaxH))) != cudaSuccess) return e;
         golden_prob_kernel<LIDX_E4M3><<<g2, 128, smem, st>>>(a, lse2);
         break;
     }
@@ -480,8 +484,8 @@ cudaError_t launch_eval(const lidx_eval_args &a, void *ws, cudaStream_t st) {
   }
   if (a.ops & LIDX_EVAL_TOPP) {
     const size_t row_bytes = static_cast<size_t>(a.N) * sizeof(float);
-    if (row_bytes <= 200u * 1024u) {
-      cudaFuncSetAttribute(topp_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(row_bytes));
+    if (row_bytes <= kMaxRowBytes) {
+      if ((e = allow_smem(topp_kernel<true>, kMaxRowBytes)) != cudaSuccess) return e;
       topp_kernel<true><<<a.L * a.T, kT, row_bytes, st>>>(a, status);
     } else {
       topp_kernel<false><<<a.L * a.T, kT, 0, st>>>(a, status);

@@ -18,6 +18,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kD = 128;
+constexpr int kMaxH = 128;
 
 // Load 8 consecutive logical dims [d0, d0+8) of key row `row` as fp32.
 template <int KT>
@@ -112,19 +113,23 @@ __global__ void __launch_bounds__(kThreads) score_cc_kernel(lidx_score_args a, i
   }
 }
 
+constexpr size_t smem_of(int Hp) { return (static_cast<size_t>(Hp) * kD + Hp) * sizeof(float); }
+
 template <int KT>
 cudaError_t launch_kt(const lidx_score_args &a, cudaStream_t st) {
   const int HG = a.H <= 16 ? 16 : 32;
   const int Hp = (a.H + HG - 1) / HG * HG;
-  const size_t smem = (static_cast<size_t>(Hp) * kD + Hp) * sizeof(float);
+  const size_t smem = smem_of(Hp);
   dim3 grid((a.N + kThreads - 1) / kThreads, a.B * a.Q);
   if (HG == 16) {
     auto k = score_cc_kernel<KT, 16>;
-    cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = allow_smem(k, smem_of(16));
+    if (e != cudaSuccess) return e;
     k<<<grid, kThreads, smem, st>>>(a, Hp);
   } else {
     auto k = score_cc_kernel<KT, 32>;
-    cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = allow_smem(k, smem_of(kMaxH));
+    if (e != cudaSuccess) return e;
     k<<<grid, kThreads, smem, st>>>(a, Hp);
   }
   return cudaGetLastError();

@@ -39,6 +39,7 @@ constexpr int kTileM = 128;
 constexpr int kTileBytes = kTileM * 128 * 2;  // bf16 [128][128] as two 64-wide swizzled panels
 constexpr int kPanelBytes = kTileBytes / 2;
 constexpr int kF8Bytes = kTileM * 64;         // raw E4M3 half-tile
+constexpr int kMaxNM = 128;                    // query columns of a group: at most 128 heads
 constexpr int kMaxGroups = 4;                 // epilogue groups of four warps (at most)
 // bf16 keys: four groups, each with its own TMEM accumulator of <= 128
 // columns; E4M3 keys: two groups (the converter warps need the registers)
@@ -455,13 +456,12 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1)
 }
 
 int sm_count() {
-  static int n = 0;
-  if (!n) {
-    int dev = 0;
+  static const int n = [] {
+    int dev = 0, sms = 0;
     cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    if (n <= 0) n = 148;
-  }
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms > 0 ? sms : 148;
+  }();
   return n;
 }
 
@@ -532,11 +532,13 @@ cudaError_t launch_score_tc(const lidx_score_args &a, cudaStream_t st) {
   const bool pdl = (a.flags & LIDX_LAUNCH_PDL) != 0;
   const int grid = static_cast<int>(std::min<long long>(p.units, sm_count()));
   if (fp8) {
-    cudaFuncSetAttribute(score_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = allow_smem(score_tc_kernel<true>, tc_smem_bytes(kMaxNM, true));
+    if (e != cudaSuccess) return e;
     return launch_kernel(score_tc_kernel<true>, dim3(grid), dim3(Roles<true>::kThreads), smem, st, pdl, tm_a,
                          tm_rope, tm_q, p);
   } else {
-    cudaFuncSetAttribute(score_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = allow_smem(score_tc_kernel<false>, tc_smem_bytes(kMaxNM, false));
+    if (e != cudaSuccess) return e;
     return launch_kernel(score_tc_kernel<false>, dim3(grid), dim3(Roles<false>::kThreads), smem, st, pdl, tm_a,
                          tm_rope, tm_q, p);
   }

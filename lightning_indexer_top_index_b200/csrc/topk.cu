@@ -27,6 +27,7 @@
 //   4. those counts' prefix gives every thread its output offset: ids come
 //      out ascending, ties to the lower index.
 #include <algorithm>
+#include <atomic>
 
 #include "kernels.cuh"
 #include "tc.cuh"
@@ -841,11 +842,12 @@ cudaError_t launch_c(int G, int rows, const SelParams &p, cudaStream_t st, bool 
 // Whether the device schedules a 16-CTA cluster of the select kernel (a
 // non-portable size), found once per device.
 bool cluster16_ok() {
-  static int cache[64] = {};  // 0 unknown, 1 yes, 2 no
+  static std::atomic<int> cache[64];  // 0 unknown, 1 yes, 2 no
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return false;
-  if (!cache[dev]) {
+  int known = cache[dev].load(std::memory_order_relaxed);
+  if (!known) {
     cudaFuncSetAttribute(select_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          static_cast<int>(select_smem<32>()));
     cudaFuncSetAttribute(select_kernel<32>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -863,9 +865,10 @@ bool cluster16_ok() {
     int n = 0;
     const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, select_kernel<32>, &cfg);
     cudaGetLastError();
-    cache[dev] = e == cudaSuccess && n >= 1 ? 1 : 2;
+    known = e == cudaSuccess && n >= 1 ? 1 : 2;
+    cache[dev].store(known, std::memory_order_relaxed);
   }
-  return cache[dev] == 1;
+  return known == 1;
 }
 
 // Cluster size and items per thread for rows of N entries.
