@@ -14,21 +14,25 @@ the argument struct, the workspace and the outputs once, and returns a
 PagedCall that enqueues the kernels each time it is called, on the current
 stream or on the one it is given.  A prepared call reads and writes the same
 tensors every time (as a CUDA graph does) and keeps them alive; one prepared
-call, like its workspace, serves one stream at a time.
+call, like its workspace, serves one stream at a time.  Preparing waits on the
+host for the current stream (unless it is being captured), so that a workspace
+and outputs made there are ready for every stream.  The memory of a call that
+was given a raw stream handle is the caller's to keep (with the call) until that
+stream's work is done; for torch's streams the allocator is told.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes as C
 import dataclasses
+import functools
 from typing import Optional
 
 import torch
 
 from . import (BF16, E2M1, E4M3, F32, LAUNCH_PDL, OP_BLOCK_POOL, OP_BLOCK_SELECT, OP_PAGED_APPEND, OP_PAGED_ATTN,
                OP_PAGED_READ, ROPE_ADJACENT, BlockPoolArgs, BlockSelectArgs, DeviceKV, LidxError, PagedAppendArgs,
-               PagedAttnArgs, PagedReadArgs, PagesArgs, launch_count, lib, read_device_status, workspace,
-               workspace_size)
+               PagedAttnArgs, PagedReadArgs, PagesArgs, launch_count, lib, read_device_status, workspace_size)
 
 
 def _need(cond, msg):
@@ -41,13 +45,20 @@ def _on(stream, device):
     return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
 
 
+def _at(device):
+    """Context in which `device` is current."""
+    here = device.type == "cuda" and torch.cuda.current_device() == device.index
+    return contextlib.nullcontext() if here else torch.cuda.device(device)
+
+
 def _scope(device, stream):
     """Context in which a one-shot call allocates and enqueues: `device` is
     current and `stream`, when given, is its stream."""
+    if stream is None:
+        return _at(device)
     es = contextlib.ExitStack()
-    es.enter_context(torch.cuda.device(device))
-    if stream is not None:
-        es.enter_context(torch.cuda.stream(_on(stream, device)))
+    es.enter_context(_at(device))
+    es.enter_context(torch.cuda.stream(_on(stream, device)))
     return es
 
 
@@ -125,15 +136,38 @@ class PagedCall:
 
     def __init__(self, name, op, args, device, out, keep, ws=None):
         self.name, self.op, self.args, self.device, self.out, self._keep = name, op, args, device, out, keep
-        with torch.cuda.device(device):
+        with _at(device):
             need = workspace_size(op, args)
-            if ws is None:
-                ws = workspace(need, device)
-            _tensor("ws", ws, torch.uint8, device)
-            self.launches = launch_count(op, args)
+            if ws is None:  # only the status word has to be clear
+                ws = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+                ws.narrow(0, 0, 256).zero_()
+        _tensor("ws", ws, torch.uint8, device)
         self.ws = ws
         self._fn, self._ref = getattr(lib(), name), C.byref(args)
         self._ws, self._bytes, self._index = ws.data_ptr(), ws.numel(), device.index
+        self._known = {torch._C._cuda_getCurrentRawStream(self._index)}  # streams that the memory made here is safe on
+
+    @functools.cached_property
+    def launches(self) -> int:
+        """Kernels that one call launches."""
+        with _at(self.device):
+            return launch_count(self.op, self.args)
+
+    def _settle(self) -> "PagedCall":
+        """Wait for the stream that the workspace and the outputs were made on."""
+        with _at(self.device):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
+        return self
+
+    def _meet(self, raw, stream):
+        """First call on a stream: the memory made here is not to be given away before its work is done."""
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        if hasattr(stream, "cuda_stream"):
+            for t in {id(t): t for t in (self.ws, *(self.out if isinstance(self.out, tuple) else (self.out,)))}.values():
+                t.record_stream(stream)
+            self._known.add(raw)
 
     def __call__(self, stream=None):
         if torch.cuda.current_device() != self._index:
@@ -143,6 +177,8 @@ class PagedCall:
             raw = torch._C._cuda_getCurrentRawStream(self._index)
         else:
             raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if raw not in self._known:
+            self._meet(raw, stream)
         rc = self._fn(self._ref, self._ws, self._bytes, raw)
         if rc:
             raise LidxError(rc, self.name)
@@ -154,11 +190,20 @@ class PagedCall:
             return read_device_status(self.ws, stream)
 
 
+def _prepared(build):
+    """`build` makes a PagedCall for the current stream; the prepared form, for any."""
+    @functools.wraps(build)
+    def call(*args, **kwargs) -> PagedCall:
+        return build(*args, **kwargs)._settle()
+    return call
+
+
 def _rows_of(seq, row, n, device):
     _tensor("seq", seq, torch.int32, device, (n,))
     _tensor("row", row, torch.int32, device, (n,))
 
 
+@_prepared
 def paged_append_call(x: torch.Tensor, cache: PagedKV, seq: torch.Tensor, row: torch.Tensor, pos: torch.Tensor = None,
                       inv_freq: torch.Tensor = None, pairs: int = ROPE_ADJACENT, *, ws=None, flags=0) -> PagedCall:
     """Prepared form of paged_append; calling it returns the workspace."""
@@ -192,9 +237,10 @@ def paged_append(x, cache: PagedKV, seq, row, pos=None, inv_freq=None, pairs: in
     if x.shape[0] == 0:
         return ws
     with _scope(cache.device, stream):
-        return paged_append_call(x, cache, seq, row, pos, inv_freq, pairs, ws=ws, flags=flags)()
+        return paged_append_call.__wrapped__(x, cache, seq, row, pos, inv_freq, pairs, ws=ws, flags=flags)()
 
 
+@_prepared
 def paged_read_call(cache: PagedKV, seq: torch.Tensor, row: torch.Tensor, dtype=torch.float32, *, out=None, ws=None,
                     flags=0) -> PagedCall:
     """Prepared form of paged_read."""
@@ -218,9 +264,10 @@ def paged_read(cache: PagedKV, seq, row, dtype=torch.float32, *, out=None, ws=No
     with _scope(cache.device, stream):
         if seq.shape[0] == 0:
             return torch.zeros((0, cache.rows.dim), dtype=dtype, device=cache.device) if out is None else out
-        return paged_read_call(cache, seq, row, dtype, out=out, ws=ws)()
+        return paged_read_call.__wrapped__(cache, seq, row, dtype, out=out, ws=ws)()
 
 
+@_prepared
 def block_pool_call(keys: PagedKV, length: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor,
                     first: torch.Tensor = None, *, ws=None, flags=0) -> PagedCall:
     """Prepared form of block_pool."""
@@ -241,9 +288,10 @@ def block_pool(keys: PagedKV, length, codes, scale, first=None, *, ws=None, stre
     below length[b]; only blocks with a row >= first[b] when `first` is given
     (those an append touched).  Returns (codes, scale)."""
     with _scope(keys.device, stream):
-        return block_pool_call(keys, length, codes, scale, first, ws=ws, flags=flags)()
+        return block_pool_call.__wrapped__(keys, length, codes, scale, first, ws=ws, flags=flags)()
 
 
+@_prepared
 def block_select_call(q: torch.Tensor, w: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor, table: torch.Tensor,
                       page_rows: int, length: torch.Tensor, k: int, *, n_first=1, n_last=2, ids=None, n_sel=None,
                       ws=None, flags=0) -> PagedCall:
@@ -278,10 +326,11 @@ def block_select(q, w, codes, scale, table, page_rows: int, length, k: int, *, n
     taken.  Returns (ids int32 [B][T][k] ascending with -1 padding, n_sel
     int32 [B][T])."""
     with _scope(q.device, stream):
-        return block_select_call(q, w, codes, scale, table, page_rows, length, k, n_first=n_first, n_last=n_last,
+        return block_select_call.__wrapped__(q, w, codes, scale, table, page_rows, length, k, n_first=n_first, n_last=n_last,
                                  ids=ids, n_sel=n_sel, ws=ws, flags=flags)()
 
 
+@_prepared
 def paged_attn_call(q: torch.Tensor, cache: PagedKV, length: torch.Tensor, blocks: torch.Tensor = None,
                     n_sel: torch.Tensor = None, scale: float = None, *, out=None, lse=None, ws=None,
                     flags=0) -> PagedCall:
@@ -319,7 +368,7 @@ def paged_attn(q, cache: PagedKV, length, blocks=None, n_sel=None, scale: float 
     those in the blocks [B][T][n] (-1 skipped; the first n_sel[b][t] when
     given).  Returns (out bfloat16 [B][T][H][512], lse float32 [B][T][H])."""
     with _scope(q.device, stream):
-        return paged_attn_call(q, cache, length, blocks, n_sel, scale, out=out, lse=lse, ws=ws, flags=flags)()
+        return paged_attn_call.__wrapped__(q, cache, length, blocks, n_sel, scale, out=out, lse=lse, ws=ws, flags=flags)()
 
 
 class PagedLayer:

@@ -13,7 +13,7 @@ import torch
 
 import _paged_ref as ref
 import lightning_indexer_top_index_b200 as L
-from test_gpu_paged import DEV, FMT, _i32, _table, _values
+from test_gpu_paged import DEV, FMT, _cache, _i32, _table, _values
 
 pytestmark = pytest.mark.gpu
 
@@ -98,3 +98,48 @@ def test_select_from_several_threads(cuda_device):
     assert not errors, f"{len(errors)} calls failed: {errors[0]}"
     for call, ids in zip(calls, want):
         assert torch.equal(call.out[0], ids)
+
+
+def _small(g, rows=500, heads=64):
+    """A cache, a query and lens of one sequence."""
+    P = 64
+    table, n_pages = _table(g, [rows], P)
+    c = _cache(g, "e2m1", 512, n_pages, P, table)
+    q = torch.from_numpy(g.standard_normal((1, 1, heads, 512)).astype(np.float32)).to(DEV).bfloat16()
+    return c, q, _i32([rows])
+
+
+def test_prepared_on_a_busy_stream(cuda_device):
+    """A call prepared on a stream with work before it, then called on another:
+    what preparing does to its memory does not come after the call."""
+    c, q, n = _small(np.random.default_rng(51))
+    seq, row = _i32([0] * 400), _i32(range(400))
+    want_rows, (want, want_lse) = L.paged_read(c, seq, row), L.paged_attn(q, c, n)
+    busy, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(busy):
+        torch.cuda._sleep(200_000_000)
+        read, attn = L.paged_read_call(c, seq, row), L.paged_attn_call(q, c, n)
+    got = read(stream=other)
+    out, lse = attn(stream=other)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want_rows)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert read.status() == 0 and attn.status() == 0
+
+
+def test_prepared_call_dropped_while_another_stream_runs_it(cuda_device):
+    """The workspace is not given away before the work on another stream that uses it is done."""
+    c, q, n = _small(np.random.default_rng(52))
+    want, _ = L.paged_attn(q, c, n)
+    call = L.paged_attn_call(q, c, n)
+    size, other = call.ws.numel(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(other):
+        torch.cuda._sleep(200_000_000)
+        out, _ = call()
+    del call
+    mine = torch.full((size,), 0x5A, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    assert (mine == 0x5A).all()
+    assert torch.equal(out, want)
