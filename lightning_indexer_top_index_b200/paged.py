@@ -14,7 +14,9 @@ the argument struct, the workspace and the outputs once, and returns a
 PagedCall that enqueues the kernels each time it is called, on the current
 stream or on the one it is given.  A prepared call reads and writes the same
 tensors every time (as a CUDA graph does) and keeps them alive; one prepared
-call, like its workspace, serves one stream at a time.  Preparing waits on the
+call, like its workspace, serves one stream at a time.  It stays with the
+tensors that a PagedKV held when it was prepared: a cache whose pool or table is
+replaced by another tensor needs its calls prepared again.  Preparing waits on the
 host for the current stream (unless it is being captured), so that a workspace
 and outputs made there are ready for every stream.  The memory of a call that
 was given a raw stream handle is the caller's to keep (with the call) until that
@@ -104,6 +106,10 @@ class PagedKV:
     @property
     def n_pages(self) -> int:
         return self.rows.rows // self.page_rows
+
+    def tensors(self) -> tuple:
+        """Those that the cache consists of now: what a prepared call keeps alive."""
+        return tuple(t for t in (self.rows.data, self.rows.scale, self.rows.rope, self.table) if t is not None)
 
     def args(self) -> PagesArgs:
         r, dev = self.rows, self.device
@@ -222,7 +228,8 @@ def paged_append_call(x: torch.Tensor, cache: PagedKV, seq: torch.Tensor, row: t
                         x.stride(0) if n > 1 else dim, cache.args(), seq.data_ptr(), row.data_ptr(),
                         None if pos is None else pos.data_ptr(), None if inv_freq is None else inv_freq.data_ptr(),
                         pairs, flags)
-    call = PagedCall("lidx_paged_append", OP_PAGED_APPEND, a, dev, None, (x, cache, seq, row, pos, inv_freq), ws)
+    call = PagedCall("lidx_paged_append", OP_PAGED_APPEND, a, dev, None, (x, *cache.tensors(), seq, row, pos, inv_freq),
+                     ws)
     call.out = call.ws
     return call
 
@@ -255,7 +262,7 @@ def paged_read_call(cache: PagedKV, seq: torch.Tensor, row: torch.Tensor, dtype=
     _need(out.stride(1) == 1 and (n == 1 or out.stride(0) >= dim), "out must have adjacent columns and rows apart")
     a = PagedReadArgs(n, cache.table.shape[0], cache.args(), seq.data_ptr(), row.data_ptr(),
                       F32 if out.dtype == torch.float32 else BF16, out.data_ptr(), out.stride(0) if n > 1 else dim, flags)
-    return PagedCall("lidx_paged_read", OP_PAGED_READ, a, dev, out, (cache, seq, row), ws)
+    return PagedCall("lidx_paged_read", OP_PAGED_READ, a, dev, out, (*cache.tensors(), seq, row), ws)
 
 
 def paged_read(cache: PagedKV, seq, row, dtype=torch.float32, *, out=None, ws=None, stream=None):
@@ -279,7 +286,7 @@ def block_pool_call(keys: PagedKV, length: torch.Tensor, codes: torch.Tensor, sc
     _tensor("scale", scale, torch.float32, dev, (keys.n_pages,))
     a = BlockPoolArgs(B, keys.args(), length.data_ptr(), None if first is None else first.data_ptr(), codes.data_ptr(),
                       scale.data_ptr(), flags)
-    return PagedCall("lidx_block_pool", OP_BLOCK_POOL, a, dev, (codes, scale), (keys, length, first), ws)
+    return PagedCall("lidx_block_pool", OP_BLOCK_POOL, a, dev, (codes, scale), (*keys.tensors(), length, first), ws)
 
 
 def block_pool(keys: PagedKV, length, codes, scale, first=None, *, ws=None, stream=None, flags=0):
@@ -358,7 +365,8 @@ def paged_attn_call(q: torch.Tensor, cache: PagedKV, length: torch.Tensor, block
                       None if blocks is None else blocks.data_ptr(), ld, ld,
                       None if n_sel is None else n_sel.data_ptr(), float(D ** -0.5 if scale is None else scale),
                       out.data_ptr(), lse.data_ptr(), flags)
-    return PagedCall("lidx_paged_attn", OP_PAGED_ATTN, a, dev, (out, lse), (q, cache, length, blocks, n_sel), ws)
+    return PagedCall("lidx_paged_attn", OP_PAGED_ATTN, a, dev, (out, lse),
+                     (q, *cache.tensors(), length, blocks, n_sel), ws)
 
 
 def paged_attn(q, cache: PagedKV, length, blocks=None, n_sel=None, scale: float = None, *, out=None, lse=None, ws=None,

@@ -5,7 +5,9 @@ streams, selections among many near scores, values that are not numbers.
 Tolerances as derived in test_gpu_paged.py, but for the probabilities: they
 enter the second product as a bf16 value and the bf16 value of what its
 rounding left, together within 2^-16 of each."""
+import gc
 import threading
+import weakref
 
 import numpy as np
 import pytest
@@ -143,3 +145,29 @@ def test_prepared_call_dropped_while_another_stream_runs_it(cuda_device):
     torch.cuda.synchronize()
     assert (mine == 0x5A).all()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "bf16"])
+def test_prepared_call_keeps_a_replaced_cache(cuda_device, fmt):
+    """A cache object may be given a longer table or a larger pool: a call that was
+    prepared before keeps the tensors that its pointers name."""
+    g = np.random.default_rng(53)
+    P, n = 64, _i32([100])
+    table, n_pages = _table(g, [100], P)
+    c, k = _cache(g, fmt, 512, n_pages, P, table), _cache(g, fmt, 128, n_pages, P, table)
+    q = torch.zeros(1, 1, 64, 512, dtype=torch.bfloat16, device=DEV)
+    codes, scale = torch.zeros(n_pages, 128, dtype=torch.int8, device=DEV), torch.zeros(n_pages, device=DEV)
+    seq = _i32([0])
+    calls = [L.paged_attn_call(q, c, n), L.paged_read_call(c, seq, seq), L.block_pool_call(k, n, codes, scale),
+             L.paged_append_call(torch.zeros(1, 512, device=DEV), c, seq, seq)]
+    held = [weakref.ref(t) for x in (c, k) for t in x.tensors()]
+    for x in (c, k):
+        x.table = x.table.clone()
+        for plane in ("data", "scale", "rope"):
+            if getattr(x.rows, plane) is not None:
+                setattr(x.rows, plane, getattr(x.rows, plane).clone())
+    gc.collect()
+    assert all(r() is not None for r in held)
+    del calls
+    gc.collect()
+    assert all(r() is None for r in held)
