@@ -15,7 +15,7 @@ import torch
 
 import _paged_ref as ref
 import lightning_indexer_top_index_b200 as L
-from test_gpu_paged import DEV, FMT, _cache, _i32, _table, _values
+from test_gpu_paged import DEV, FMT, _cache, _i32, _select, _table, _values
 
 pytestmark = pytest.mark.gpu
 
@@ -55,6 +55,53 @@ def test_attn_probabilities_keep_16_bits(cuda_device, fmt, rows, heads):
     out, _ = L.paged_attn(q.to(DEV)[None, None], c, _i32([rows]), scale=1.0)
     worst = (np.abs(out.cpu().double().numpy() - want[0]) / attn_bound(want, rows)).max()
     assert worst <= 1.0, f"out off by {worst:.2f} of its bound"
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3", "bf16"])
+@pytest.mark.parametrize("rows,bad", [(50, [3]), (50, range(50)), (700, [0]), (700, [650]), (700, range(64))])
+def test_attn_nan_in_an_attended_row(cuda_device, fmt, rows, bad):
+    """A NaN in a row that is attended to reaches all heads and dims, whether the job
+    is one chunk or split over CTAs, also where a chunk holds nothing else; the
+    batch's other sequence stays as it was."""
+    g = np.random.default_rng(60 + rows)
+    P, lens, H = 64, [rows, 130], 70
+    table, n_pages = _table(g, lens, P)
+    c = _cache(g, fmt, 512, n_pages, P, table)
+    q = torch.from_numpy(g.standard_normal((2, 1, H, 512)).astype(np.float32)).to(DEV).bfloat16()
+    clean, clean_lse = L.paged_attn(q, c, _i32(lens))
+    at = [int(table[0, r // P]) * P + r % P for r in bad]
+    if fmt == "bf16":
+        c.rows.data[at, 100] = float("nan")
+    else:
+        c.rows.scale[at, 2] = 0xFF
+    out, lse = L.paged_attn(q, c, _i32(lens))
+    assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all()
+    assert torch.equal(out[1], clean[1]) and torch.equal(lse[1], clean_lse[1])
+
+
+@pytest.mark.parametrize("rows", [40, 700])
+def test_attn_infinite_value(cuda_device, rows):
+    """A row with an infinite value: heads whose score of it is -inf lose that dim
+    only (0 * inf), the others are NaN, as the formula has it."""
+    g = np.random.default_rng(61)
+    P, lens = 64, [rows]
+    table, n_pages = _table(g, lens, P)
+    c = _cache(g, "bf16", 512, n_pages, P, table)
+    c.rows.data[int(table[0, 0]) * P + 7, 33] = float("inf")
+    q = torch.from_numpy(g.standard_normal((1, 1, 64, 512)).astype(np.float32)).to(DEV).bfloat16()
+    out, lse = L.paged_attn(q, c, _i32(lens))
+    vals, qn = _values(c, "bf16"), q.double().cpu().numpy()
+    with np.errstate(all="ignore"):
+        want, want_lse, _, _ = ref.attend(qn, vals, table, P, n_pages, lens, 512 ** -0.5)
+    assert np.array_equal(torch.isnan(out).cpu().numpy(), np.isnan(want))
+    assert np.array_equal(torch.isnan(lse).cpu().numpy(), np.isnan(want_lse))
+    assert 0 < np.isnan(want_lse).sum() < 64
+    # where its probability is 0, the values are those of the other rows
+    others = np.zeros((n_pages * P, 512))
+    others[: rows - 1] = vals[[int(table[0, r // P]) * P + r % P for r in range(rows) if r != 7]]
+    without = ref.attend(qn, others, np.arange(n_pages, dtype=np.int32)[None], P, n_pages, [rows - 1], 512 ** -0.5)
+    off = np.abs(out.double().cpu().numpy() - without[0]) / attn_bound(without, rows)
+    assert off[~np.isnan(want)].max() <= 1.0
 
 
 # ------------------------------------------------- several threads and streams
@@ -171,3 +218,41 @@ def test_prepared_call_keeps_a_replaced_cache(cuda_device, fmt):
     del calls
     gc.collect()
     assert all(r() is None for r in held)
+
+
+# ------------------------------------------------------------------ select
+def near_scores(g, kind, n):
+    """Block scales, to which the scores are in proportion: a few far ones
+    stretch the range, so that most of the others share a bin of it."""
+    near = {"near": lambda: 1.0 + g.random(n) * 2.0 ** -7, "infinite": lambda: g.random(n),
+            "signs": lambda: (g.random(n) - 0.5) * 2.0 ** -5,
+            "low bits": lambda: 1.0 + g.integers(0, 4 * n, n) * 2.0 ** -23,
+            "duplicates": lambda: np.where(g.random(n) < 0.4, 1.0 + 2.0 ** -9, 1.0 + g.random(n) * 1.01 * 2.0 ** -9)}[kind]()
+    far = g.permutation(n)[:4]
+    near[far] = [1000.0, -1000.0, 999.0, 998.5] if kind != "infinite" else [np.inf, -np.inf, np.inf, 5.0]
+    return near.astype(np.float32)
+
+
+NEAR = [(kind, *size) for kind in ("near", "signs", "low bits", "duplicates", "infinite")
+        for size in ((1, 20000, 16), (2, 20000, 256), (80, 3001, 40), (10, 40000, 250))]
+
+
+def near_case(kind, B, n_blocks, k):
+    g = np.random.default_rng(n_blocks + k + len(kind))
+    scale = near_scores(g, kind, n_blocks)
+    codes = np.full((n_blocks, 128), 3, np.int8)
+    table = np.stack([g.permutation(n_blocks) for _ in range(B)]).astype(np.int32)
+    q, w = np.ones((B, 1, 1, 128), np.float32), g.random((B, 1, 1)).astype(np.float32) + 0.1
+    return q, w, codes, scale, table
+
+
+@pytest.mark.parametrize("kind,B,n_blocks,k", NEAR)
+def test_select_near_scores(cuda_device, kind, B, n_blocks, k):
+    """More than 256 scores in the bin of the k-th: the digits of the scores decide, down to the last
+    where many are equal, in a CTA's slice of a row and among the lists of a cluster."""
+    q, w, codes, scale, table = near_case(kind, B, n_blocks, k)
+    lens = [16 * n_blocks] * B
+    ids, n_sel, status, qb = _select(q, w, codes, scale, table, 16, lens, k)
+    want, wn = ref.select(qb, w, codes, scale, table, 16, n_blocks, lens, k, 1, 2)
+    assert status == 0 and np.array_equal(n_sel, wn)
+    assert np.array_equal(ids, want)
