@@ -499,7 +499,8 @@ LIDX_API lidx_status lidx_block_pool(const lidx_block_pool_args *args, void *ws,
  * are the sequence's last T rows), so the blocks j < nb = ceil(v/page_rows).
  *   sq[h]    = top * (1/127),                 top = max_d |q[b,t,h,d]|
  *   qi[h,d]  = rint(q[b,t,h,d] * (127 * (1/top)))     (0 when top is 0; every
- *              operation of these two rounded to fp32)
+ *              operation of these two rounded to fp32; for a top below 2^-100
+ *              qi is that of 2^100 q and 2^100 top, as 127/top may overflow)
  *   score[j] = (sum_h (w[b,t,h] * sq[h]) * max(qi[h] . codes[p_j], 0)) * scale[p_j]
  * with the dot products in whole numbers, w * sq rounded to fp32 and the rest
  * in 64 bits, so that the ranking is the formula's and does not depend on the

@@ -436,7 +436,13 @@ __global__ void __launch_bounds__(kThreads, 2) block_select_kernel(const lidx_bl
     if (nan) top = __uint_as_float(0x7FC00000u);
     const bool bad = __shfl_xor_sync(0xFFFFFFFFu, nan, 1) | nan;
     if (__shfl_xor_sync(0xFFFFFFFFu, bad, 2) | bad) top = __uint_as_float(0x7FC00000u);
-    const float inv = top > 0.f ? __fmul_rn(__frcp_rn(top), 127.f) : 0.f;
+    float unit = top;
+    if (top < 0x1p-100f) {  // 127 / top would leave the range of fp32
+      unit *= 0x1p100f;
+#pragma unroll
+      for (int i = 0; i < 32; i++) v[i] *= 0x1p100f;
+    }
+    const float inv = unit > 0.f ? __fmul_rn(__frcp_rn(unit), 127.f) : 0.f;
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) {

@@ -15,7 +15,7 @@ import torch
 
 import _paged_ref as ref
 import lightning_indexer_top_index_b200 as L
-from test_gpu_paged import DEV, FMT, _cache, _i32, _select, _table, _values
+from test_gpu_paged import DEV, FMT, _cache, _i32, _select, _summaries, _table, _values
 
 pytestmark = pytest.mark.gpu
 
@@ -256,3 +256,27 @@ def test_select_near_scores(cuda_device, kind, B, n_blocks, k):
     want, wn = ref.select(qb, w, codes, scale, table, 16, n_blocks, lens, k, 1, 2)
     assert status == 0 and np.array_equal(n_sel, wn)
     assert np.array_equal(ids, want)
+
+
+@pytest.mark.parametrize("exponent", [-99, -101, -119, -122, -128, -131])
+def test_select_tiny_queries(cuda_device, exponent):
+    """Queries whose largest magnitudes are so small that 127 over them overflows, down to
+    subnormals of bf16: the ids are those of the formula with both scaled by 2^100."""
+    g = np.random.default_rng(exponent + 500)
+    n, H, k, P = 400, 8, 12, 16
+    codes, scale = _summaries(g, n)
+    table = g.permutation(n).astype(np.int32)[None]
+    q = torch.from_numpy((g.standard_normal((1, 1, H, 128)) * 2.0 ** exponent).astype(np.float32)).bfloat16().float().numpy()
+    w = (g.random((1, 1, H)) + 0.5).astype(np.float32) * np.float32(2.0 ** 100)  # w * sq a normal number
+    ids, n_sel, status, qb = _select(q, w, codes, scale, table, P, [n * P], k, n_first=0, n_last=0)
+    assert np.array_equal(qb, q)
+    top = np.abs(q[0, 0]).max(1)
+    up = np.where(top < 2.0 ** -100, np.float32(2.0 ** 100), np.float32(1))
+    inv = np.float32(127) * (np.float32(1) / (top * up))
+    qi = np.rint((q[0, 0] * up[:, None]) * inv[:, None])
+    assert np.abs(qi).max() == 127
+    weight = (w[0, 0] * (top * (np.float32(1) / np.float32(127)))).astype(np.float64)
+    dot = np.maximum(qi @ codes[table[0]].astype(np.float64).T, 0)
+    score = (dot * weight[:, None]).sum(0) * scale[table[0]].astype(np.float64)
+    want = np.sort(np.argsort(-score, kind="stable")[:k])
+    assert status == 0 and n_sel[0, 0] == k and np.array_equal(ids[0, 0], want)
