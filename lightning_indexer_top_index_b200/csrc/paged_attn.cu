@@ -1120,7 +1120,8 @@ cudaError_t launch(const CUtensorMap &tm, const lidx_paged_attn_args &a, const J
 
 bool paged_attn_supported(const lidx_paged_attn_args &a) {
   const int64_t rows = static_cast<int64_t>(a.blocks ? a.n_blocks : a.cache.max_pages) * a.cache.page_rows;
-  return rows <= INT32_MAX && job_count(a) <= (1 << 24) && job_count(a) * most_chunks(a) <= INT32_MAX;
+  // entries of a job are counted in 32 bits up to the end of its last chunk
+  return rows <= INT32_MAX - (kRows - 1) && job_count(a) <= (1 << 24) && job_count(a) * most_chunks(a) <= INT32_MAX;
 }
 
 size_t paged_attn_workspace(const lidx_paged_attn_args &a) {
