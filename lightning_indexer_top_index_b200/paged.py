@@ -392,8 +392,10 @@ class PagedLayer:
 
     def __init__(self, rows: PagedKV, keys: PagedKV, H: int, k: int, T: int = 1, *, n_first: int = 1, n_last: int = 2,
                  inv_freq: torch.Tensor = None, pairs: int = ROPE_ADJACENT, scale: float = None, pdl: bool = True):
-        _need(rows.page_rows == keys.page_rows and rows.n_pages == keys.n_pages and
-              rows.table.data_ptr() == keys.table.data_ptr(), "rows and keys must share pages and table")
+        a, b = rows.table, keys.table
+        _need(rows.page_rows == keys.page_rows and rows.n_pages == keys.n_pages and a.device == b.device and
+              a.data_ptr() == b.data_ptr() and a.shape == b.shape and a.stride() == b.stride(),
+              "rows and keys must share pages and table")
         dev, B = rows.device, rows.table.shape[0]
         self.rows, self.keys, self.B, self.T = rows, keys, B, T
         flags = LAUNCH_PDL if pdl else 0  # every paged call waits for its predecessor before it reads anything
@@ -423,9 +425,12 @@ class PagedLayer:
         """One step's data (host pinned or device): the new rows [B*T][512] and
         keys [B*T][128], the queries, the rows each sequence held before this
         step (length, int32 [B]) and the rotary positions (default: the rows)."""
-        T = self.T
-        for dst, src in ((self.x_rows, x_rows), (self.x_keys, x_keys), (self.q_idx, q_idx), (self.w, w),
-                         (self.q_attn, q_attn), (self.first, length)):
+        T, pos_in = self.T, () if pos is None else (("pos", self.pos, pos),)
+        given = (("x_rows", self.x_rows, x_rows), ("x_keys", self.x_keys, x_keys), ("q_idx", self.q_idx, q_idx),
+                 ("w", self.w, w), ("q_attn", self.q_attn, q_attn), ("length", self.first, length))
+        for name, dst, src in (*given, *pos_in):  # a copy would spread a smaller one over the batch
+            _need(src.shape == dst.shape, f"{name} must be {tuple(dst.shape)}, got {tuple(src.shape)}")
+        for _, dst, src in given:
             dst.copy_(src, non_blocking=non_blocking)
         torch.add(self.first, T, out=self.length)
         at = self.first.unsqueeze(1) + torch.arange(T, dtype=torch.int32, device=self.first.device)
