@@ -466,7 +466,8 @@ LIDX_API lidx_status lidx_paged_read(const lidx_paged_read_args *args, void *ws,
  *   mean[d]     = sum_r key_r[d] / count            (64-bit sums)
  *   scale[p]    = fp32(max_d |mean[d]| / 127)
  *   codes[p][d] = rint(mean[d] / scale[p])          (ties to even; 0 when the
- *                                                    scale is 0)
+ *                                                    scale is 0; cut to +-127,
+ *                                                    where the scale is subnormal)
  *
  * for every block with rows, or, with `first`, those that hold a row >=
  * first[b] (the blocks that an append touched).  Summaries are kept by page,
@@ -475,7 +476,7 @@ LIDX_API lidx_status lidx_paged_read(const lidx_paged_read_args *args, void *ws,
  * mean gets scale NaN and codes 0 (never selected by its score) and sets
  * LIDX_DEV_NAN; lens beyond the table are cut to it and set LIDX_DEV_BOUNDS.
  *   keys   dim 128: LIDX_F32 | LIDX_BF16 | LIDX_E4M3 | LIDX_E2M1
- *   len    [B] int32; first [B] int32 (optional)
+ *   len    [B] int32, B <= 65535; first [B] int32 (optional)
  *   codes  [n_pages][128] int8, 16-byte aligned; scale [n_pages] fp32
  * Needs lidx_workspace_size(LIDX_OP_BLOCK_POOL) bytes (the status word).
  * ------------------------------------------------------------------------ */
@@ -514,8 +515,8 @@ LIDX_API lidx_status lidx_block_pool(const lidx_block_pool_args *args, void *ws,
  *   codes, scale as lidx_block_pool writes them (summaries of n_pages pages)
  *   ids    [B][T][k] int32: the taken blocks in ascending order, then -1
  *   n_sel  [B][T] int32 (optional): how many were taken
- * k in [1, 256], n_first + n_last <= k, at most 131072 blocks a sequence
- * (larger: LIDX_ERR_UNSUPPORTED).  lens beyond the table are cut to
+ * k in [1, 256], n_first + n_last <= k, at most 131072 blocks a sequence and
+ * 2^24 queries (larger: LIDX_ERR_UNSUPPORTED).  lens beyond the table are cut to
  * it and set LIDX_DEV_BOUNDS.  Needs
  * lidx_workspace_size(LIDX_OP_BLOCK_SELECT) bytes.
  * ------------------------------------------------------------------------ */

@@ -11,8 +11,9 @@
 // lane by four lanes and their angles fetched by shuffles, 20011 rows of 512,
 // appended and read back, took 28.4 us instead of 25.6.  An angle is formed as
 // pos * inv_freq / 2 pi turns in 64 bits and its whole turns dropped before it
-// is rounded to fp32 (error below 2^-25 turns at any position), since in fp32
-// the product alone would be off by up to pos * 2^-24 radians.
+// is rounded to fp32 (error below 2^-25 turns up to 2^25 of them, from there on
+// 2^-51 of the turns), since in fp32 the product alone would be off by up to
+// pos * 2^-24 radians.
 #include "paged.cuh"
 #include "quant.cuh"
 
@@ -229,9 +230,9 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const lidx_paged
 }
 
 // Rows as values: dim/8 threads a row, thread t dims [8t, 8t + 8), kPer rows of
-// it in flight together.  The instructions bound it: as bf16 the values come
-// from bf16 products of code and scale (through fp32, and rounded with a look
-// for NaNs, the 20011 rows took 3 us more).
+// it in flight together.  Instructions and loads bound it (65 % of the issue
+// slots): as bf16 the values come from bf16 products of code and scale (through
+// fp32, and rounded with a look for NaNs, the 20011 rows took 3 us more).
 template <int kFmt, int kPer>
 __global__ void __launch_bounds__(kThreads) paged_read_kernel(const lidx_paged_read_args a, int shift,
                                                                uint32_t *status) {

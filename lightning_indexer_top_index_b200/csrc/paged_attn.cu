@@ -39,11 +39,11 @@
 //   that rounding left, so it keeps 16 bits (2^-16 of each probability), as in
 //   the attention over linear caches; both are products of the same rows.
 //
-// What bounds it.  For 256 queries of 1024 rows in E2M1 (86 us, 20 at the bf16
-// rate of the matrix products) a CTA takes a chunk every 3700 cycles.  Its
+// What bounds it.  For 256 queries of 1024 rows in E2M1 (84 us, 20 at the bf16
+// rate of the matrix products) a CTA takes a chunk every 3500 cycles.  Its
 // products (32 of 32 cycles, 32 of 48, both bound by their operands in shared
 // memory) take 2560 of them; a loader warp, always busy, takes all of them for
-// its 550 instructions, with half of all issue slots used, 9000 instructions a
+// its 550 instructions, with 45 % of all issue slots used, 7800 instructions a
 // chunk, a quarter of them in the expansion.  Sixteen loader warps of half as
 // much each leave the others fewer slots and registers: 94 us.
 //
