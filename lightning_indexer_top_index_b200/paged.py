@@ -388,7 +388,9 @@ class PagedLayer:
     The step owns its inputs and outputs; `set_inputs` copies a step's data
     in, `enqueue` issues the five calls, `capture` records them as a CUDA
     graph that `replay` launches.  rows: PagedKV of dim 512; keys: PagedKV of
-    dim 128 on the same table."""
+    dim 128 on the same table; H index heads and as many attention heads, up to
+    64.  Every sequence takes part in a step: a batch with idle ones, or with
+    other counts of heads, uses the calls themselves."""
 
     def __init__(self, rows: PagedKV, keys: PagedKV, H: int, k: int, T: int = 1, *, n_first: int = 1, n_last: int = 2,
                  inv_freq: torch.Tensor = None, pairs: int = ROPE_ADJACENT, scale: float = None, pdl: bool = True):
