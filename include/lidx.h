@@ -552,7 +552,7 @@ LIDX_API lidx_status lidx_block_select(const lidx_block_select_args *args, void 
  *
  *   q     [B][T][H][512] bf16, 16-byte aligned, H <= 128
  *   cache dim 512, LIDX_E2M1 | LIDX_E4M3 | LIDX_BF16
- *   out   [B][T][H][512] bf16
+ *   out   [B][T][H][512] bf16;  scale in [-1e38, 1e38]
  * A query's rows (max_pages, or n_blocks, times page_rows) number at most
  * 2^31 - 64, the queries times ceil(H/64) at most 2^24, and these times the
  * chunks of 64 rows less than 2^31 (larger: LIDX_ERR_UNSUPPORTED).

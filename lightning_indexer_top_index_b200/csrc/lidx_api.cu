@@ -251,7 +251,7 @@ lidx_status check_paged_attn(const lidx_paged_attn_args *a) {
   if (a->blocks && (!readable(a->blocks) || a->n_blocks < 1 || a->ld_blocks < a->n_blocks ||
                     (a->n_sel && !readable(a->n_sel))))
     return LIDX_ERR_INVALID_ARG;
-  if (!(a->scale == a->scale) || a->scale == INFINITY || a->scale == -INFINITY) return LIDX_ERR_INVALID_ARG;
+  if (!(a->scale >= -1e38f && a->scale <= 1e38f)) return LIDX_ERR_INVALID_ARG;  // log2(e) times it is finite
   lidx_status s = check_pages(a->cache, 512, a->B);
   if (s != LIDX_OK) return s;
   if (a->H > 128 || a->cache.rows.dtype == LIDX_F32) return LIDX_ERR_UNSUPPORTED;

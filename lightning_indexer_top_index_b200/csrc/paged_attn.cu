@@ -13,7 +13,7 @@
 //     four chunks ahead and says where a job begins and ends;
 //   * eight loader warps, eight rows each, fetch the stored rows a chunk ahead
 //     into registers, expand them to bf16 (exact: every E2M1 or E4M3 value
-//     times a power of two is a bf16 value) and store them as the swizzled
+//     times a power of two is a bf16 value while it is in its range) and store them as the swizzled
 //     K-major tile X[64 rows][512], two of which are in shared memory.  Rows
 //     that are not attended to are stored as zeros.  They go by quarters of 128
 //     dims, and S begins with the half of the dims that is in while the other
@@ -691,10 +691,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (cut && tid == 0) raise_status(ws.status, LIDX_DEV_BOUNDS);
     }
     const int half = warp >> 2, h0 = (warp & 3) * 16 + (lane >> 2), h1 = h0 + 8;  // this lane's heads
-    // logits are s * c2 in base 2; with a negative scale s changes sign instead, and a zero one
-    // becomes one that makes every product round away (0 * -inf would be NaN)
-    const bool negative = a.scale < 0.f;
-    const float c2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
+    // logits are s * c2 in base 2, c2 > 0: with a negative scale s changes sign instead, and with a
+    // zero one it becomes zero (rows that are not attended to have -inf, and 0 * -inf would be NaN)
+    const float sign = a.scale > 0.f ? 1.f : a.scale < 0.f ? -1.f : 0.f;
+    const float c2 = sign == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
     const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
     // the reference maximum is the same in both halves; the sums are of this half's rows
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
@@ -737,13 +737,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           s1[u] = __uint_as_float(x[k + 2]);
         }
       }
-      if (negative || valid != 0xFFFFFFFFu) {
+      if (sign != 1.f || valid != 0xFFFFFFFFu) {
         const uint32_t bits = valid >> (2 * (lane & 3));
 #pragma unroll
         for (int u = 0; u < 8; u++) {
           const bool in = (bits >> (8 * (u >> 1) + (u & 1))) & 1u;
-          s0[u] = in ? (negative ? -s0[u] : s0[u]) : -INFINITY;
-          s1[u] = in ? (negative ? -s1[u] : s1[u]) : -INFINITY;
+          s0[u] = in ? s0[u] * sign : -INFINITY;
+          s1[u] = in ? s1[u] * sign : -INFINITY;
         }
       }
       float t0 = s0[0], t1 = s1[0];

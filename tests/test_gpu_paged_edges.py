@@ -104,6 +104,22 @@ def test_attn_infinite_value(cuda_device, rows):
     assert off[~np.isnan(want)].max() <= 1.0
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.0, 2.0 ** -130, -2.0 ** -140])
+def test_attn_scale_of_nothing(cuda_device, scale):
+    """A zero scale makes every logit zero however large the products are, and a tiny one keeps its share."""
+    g = np.random.default_rng(62)
+    P, lens = 64, [300]
+    table, n_pages = _table(g, lens, P)
+    c = _cache(g, "bf16", 512, n_pages, P, table)
+    c.rows.data.mul_(2.0 ** 59)
+    q = torch.from_numpy((g.standard_normal((1, 1, 64, 512)) * 2.0 ** 60).astype(np.float32)).to(DEV).bfloat16()
+    out, lse = L.paged_attn(q, c, _i32(lens), scale=scale)
+    want = ref.attend(q.double().cpu().numpy(), _values(c, "bf16"), table, P, n_pages, lens, float(np.float32(scale)))
+    assert (np.abs(out.double().cpu().numpy() - want[0]) <= attn_bound(want, lens[0])).all()
+    d = 512 * 2.0 ** -24 * want[3]
+    assert (np.abs(lse.double().cpu().numpy() - want[1]) <= d + 2.0 ** -20 * (1 + np.abs(want[1]))).all()
+
+
 # ------------------------------------------------- several threads and streams
 def _many_threads(calls, times):
     """Every call `times` times, each from a thread and on a stream of its own; the errors."""

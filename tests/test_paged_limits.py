@@ -30,6 +30,13 @@ def test_rows_of_a_query(lib, pages, status):  # noqa: F811
         L.ERR_WORKSPACE if status == L.OK else status)
 
 
+@pytest.mark.parametrize("scale,status", [(1e38, L.OK), (-1e38, L.OK), (0.0, L.OK), (2e38, L.ERR_INVALID_ARG),
+                                          (-3e38, L.ERR_INVALID_ARG)])
+def test_attention_scale(lib, scale, status):  # noqa: F811
+    """log2(e) times the scale stays finite."""
+    assert _status(lib, _attn(scale=scale)) == status
+
+
 def _cache(dim, table):
     return L.PagedKV(L.DeviceKV(L.BF16, dim, torch.zeros(64, dim, dtype=torch.bfloat16)), table, 16)
 
